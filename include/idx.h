@@ -203,11 +203,103 @@ IDX_API int kmeans_scores(idx_ctx* ctx, const uint16_t* x, const uint16_t* centr
                           int D, float* scores, idx_stream stream);
 
 /*
+ * 8-bit paged KV cache: the cache of one attention layer, its block tables,
+ * its writer, and the attention that reads the pages the calls above select.
+ *
+ *   k_cache, v_cache  codes [n_blocks][H][P][D], 16-byte aligned: a block is a
+ *                     page of P keys for each of H kv heads, in IDX_KV_E4M3
+ *                     (8-bit floats, largest 448) or IDX_KV_INT8
+ *   k_scale, v_scale  fp32 [n_blocks][H], finite and not negative: a code
+ *                     stands for code * scale of its block and head
+ *   page_table        int32 [B][ld_pt], ld_pt >= N: page p of request b is
+ *                     block page_table[b][p], as in the paged calls above; the
+ *                     key at position i is row i % P of page i / P
+ *   slot              block * P + row of a token, -1 for none
+ *
+ * D a multiple of 16 and at most 256; n_blocks * H * P and N * P below 2^31.
+ * The limits given to idx_init do not bind these calls.  Their batches are
+ * [B][T] rows, T tokens per request; a request with fewer is padded (slot -1,
+ * key count 0).
+ */
+typedef enum { IDX_KV_E4M3 = 0, IDX_KV_INT8 = 1 } idx_kv_format;
+
+/*
+ * Block tables and slot maps on the device.  Request b has cached[b] keys in
+ * its pages and gets fresh[b] <= T more (fresh NULL: T each).  The pages it
+ * needs beyond the ceil(cached/P) it has are the next entries of free_list
+ * (int32 [n_free] block ids), requests in order, from entry free_head[0] on
+ * (device int32, NULL: 0); they are written into page_table.  Then
+ *     slots[b][t]       = the slot of position cached[b] + t,
+ *     key_counts[b][t]  = cached[b] + t + 1    (what kv_attention takes),
+ *     page_counts[b][t] = ceil(key_counts[b][t] / P)  (the token_lengths of the
+ *                         _tokens calls),
+ * and -1, 0, 0 for t >= fresh[b].  free_head_out (device int32, may be NULL,
+ * must not be free_head) gets the entry after the last one taken: the same
+ * call twice with the same inputs gives the same result.
+ * Reported by idx_get_status: a count outside [0, N*P] (or beyond T, or a
+ * free_head outside the list) is clamped (bit 1); a block id outside
+ * [0, n_blocks) (bit 4) or a page past the end of the free list (bit 8, its
+ * table entry becomes -1) leaves its tokens without a slot: -1, 0, 0.
+ */
+IDX_API int kv_block_tables(idx_ctx* ctx, const int32_t* cached, const int32_t* fresh, int B, int T,
+                            int P, int N, int32_t* page_table, int64_t ld_pt, int n_blocks,
+                            const int32_t* free_list, int n_free, const int32_t* free_head,
+                            int32_t* free_head_out, int32_t* slots, int32_t* key_counts,
+                            int32_t* page_counts, idx_stream stream);
+
+/*
+ * Write new keys and values, bf16 rows k + r*ldk + h*D and v + r*ldv + h*D
+ * (strides multiples of 8, 16-byte aligned), to the slots slots[r], r < R;
+ * rows of slot -1 are skipped (any other slot outside the cache too, bit 4).
+ * Per page and head, K and V apart: with a the largest finite magnitude of the
+ * page's new rows and QMAX 448 or 127,
+ *     scale = the least power of two (at least 2^-100) with QMAX*scale >= a,
+ *     or the page's old scale if that is larger and row 0 of the page is not
+ *     among the new rows;
+ * a scale that grows re-rounds the codes of the rows before the new ones,
+ * code = rne(code * (old / new)), the ratio in fp32; the new codes are rne(x / scale), infinities
+ * saturated, NaN the e4m3 code 0x7F and 0 in int8.  Other rows of the cache
+ * are left as they were.  The new rows of one page must be consecutive rows of
+ * the call at rising, adjacent slots (what kv_block_tables gives); two runs of
+ * rows for one page in one call leave its codes undefined.
+ */
+IDX_API int kv_append(idx_ctx* ctx, const uint16_t* k, const uint16_t* v, int64_t ldk, int64_t ldv,
+                      const int32_t* slots, int R, int H, int D, int P, int n_blocks, int format,
+                      void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                      idx_stream stream);
+
+/*
+ * Attention over the cache.  q: bf16, head h of row r = b*T + t at
+ * q + r*ldq + h*D (ldq a multiple of 8, q 16-byte aligned); H divides Q and
+ * query head h reads kv head h / (Q/H).  Row r sees the keys at positions
+ * below key_counts[r] (device int32 [B*T]) of the pages page_idx[r][0..K-1]
+ * (int32 [B*T][K], -1 entries skipped: idx_out of the select calls), or of all
+ * its pages when page_idx is NULL (K = 0):
+ *     s_i = scale * sum_d q_d * k_id,  out = sum_i softmax(s)_i * v_i,
+ *     lse = log(sum_i exp(s_i)).
+ * A page listed twice counts twice.  A row without keys gets out 0 and lse
+ * -inf; keys it does not see are never part of its result, whatever their
+ * codes are.  out: bf16 [B*T][Q][D], 16-byte aligned; lse: fp32 [B*T][Q] or
+ * NULL.  Sums and softmax statistics are fp32; the softmax weights are rounded
+ * once to fp16 for the products with V.
+ * Reported by idx_get_status: a key count outside [0, N*P] is clamped (bit 1);
+ * a page_idx entry outside [-1, N) or a block outside [0, n_blocks) is left
+ * out (bit 4).
+ */
+IDX_API int kv_attention(idx_ctx* ctx, const uint16_t* q, int64_t ldq, const void* k_cache,
+                         const void* v_cache, const float* k_scale, const float* v_scale,
+                         int n_blocks, int format, const int32_t* page_table, int64_t ld_pt, int N,
+                         const int32_t* key_counts, const int32_t* page_idx, int K, int B, int T,
+                         int Q, int H, int D, int P, float scale, uint16_t* out, float* lse,
+                         idx_stream stream);
+
+/*
  * Device-side status of the context: waits for `stream`, reads and clears the
  * status word.  Returns IDX_OK, or IDX_EDEVICE with *bits (if non-NULL) set to
  * the raised bits: 1 = a length outside [0, N] was clamped, 2 = a bounded wait
  * inside a kernel expired (that call's output is not valid), 4 = a page-table
- * entry outside the block pool was clamped.  Synchronises.
+ * entry outside the block pool was clamped or left out, 8 = a free list ended
+ * before every new page had a block.  Synchronises.
  */
 IDX_API int idx_get_status(idx_ctx* ctx, idx_stream stream, int* bits);
 

@@ -44,6 +44,11 @@ SIGNATURES = {
     "topk_select_noalloc": (_I, [_P, _P, _I, _I, _L, _I, _P, _P, _P]),
     "kmeans_assign": (_I, [_P, _P, _P, _I, _I, _I, _P, _P, _P]),
     "kmeans_scores": (_I, [_P, _P, _P, _I, _I, _I, _P, _P]),
+    "kv_block_tables": (_I, [_P, _P, _P, _I, _I, _I, _I, _P, _L, _I, _P, _I, _P, _P, _P, _P, _P,
+                             _P]),
+    "kv_append": (_I, [_P, _P, _P, _L, _L, _P, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "kv_attention": (_I, [_P, _P, _L, _P, _P, _P, _P, _I, _I, _P, _L, _I, _P, _P, _I, _I, _I, _I,
+                          _I, _I, _I, ctypes.c_float, _P, _P, _P]),
 }
 
 _lib = None
@@ -309,3 +314,124 @@ def score_topk_fused_paged(ctx, q, pool, page_table, lengths, K, idx_out, val_ou
                                         _ptr(val_out), _stream(stream, q.device)),
            "score_topk_fused_paged")
     return idx_out, val_out
+
+
+# 8-bit paged KV cache (see idx.h).  The format of a cache is its tensors' dtype.
+KV_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+
+
+def _kv_tensor(ctx, name, t, dtypes, shape, contiguous=True):
+    """t, checked: on the context's device, of one of the dtypes and of the shape
+    (None: any size)."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if t.device.type != "cuda" or t.device.index != ctx.device:
+        raise ValueError("%s must be on cuda:%d" % (name, ctx.device))
+    if t.dtype not in dtypes:
+        raise ValueError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError("%s must be of shape %s" % (name, tuple("*" if n is None else n for n in shape)))
+    if contiguous and not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
+def _kv_rows(name, t, lead):
+    """The row stride of t [..rows][heads][D] whose rows are contiguous and evenly spaced."""
+    heads, D = t.shape[-2:]
+    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != D):
+        raise ValueError("%s's rows must be contiguous" % name)
+    ld = None
+    for d in range(lead - 1, -1, -1):  # dimensions of one row tell nothing
+        if t.shape[d] > 1:
+            below = 1
+            for n in t.shape[d + 1:lead]:
+                below *= n
+            if t.stride(d) % below or ld not in (None, t.stride(d) // below):
+                raise ValueError("%s's rows must be evenly spaced" % name)
+            ld = t.stride(d) // below
+    return heads * D if ld is None else ld
+
+
+def _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale):
+    _kv_tensor(ctx, "k_cache", k_cache, tuple(KV_FORMATS), (None,) * 4)
+    _kv_tensor(ctx, "v_cache", v_cache, k_cache.dtype, k_cache.shape)
+    _kv_tensor(ctx, "k_scale", k_scale, torch.float32, k_cache.shape[:2])
+    _kv_tensor(ctx, "v_scale", v_scale, torch.float32, k_cache.shape[:2])
+    return (*k_cache.shape, KV_FORMATS[k_cache.dtype])
+
+
+def kv_block_tables(ctx, cached, fresh, P, n_blocks, page_table, free_list, free_head,
+                    free_head_out, slots, key_counts, page_counts, stream=None):
+    """Pages for fresh[b] (None: T) new tokens behind cached[b] keys, taken from free_list from
+    entry free_head[0] (None: 0) on and written into page_table [B][N]; slots, key_counts and
+    page_counts [B][T] of the new tokens; free_head_out[0] (may be None) = the entry after the
+    last one taken.  All tensors int32."""
+    i32 = torch.int32
+    _kv_tensor(ctx, "slots", slots, i32, (None, None))
+    B, T = slots.shape
+    _kv_tensor(ctx, "cached", cached, i32, (B,))
+    _kv_tensor(ctx, "page_table", page_table, i32, (B, None), contiguous=False)
+    if page_table.stride(1) != 1 or (B > 1 and page_table.stride(0) < page_table.shape[1]):
+        raise ValueError("page_table's rows must be contiguous")
+    _kv_tensor(ctx, "free_list", free_list, i32, (None,))
+    for name, t, shape in (("fresh", fresh, (B,)), ("free_head", free_head, (1,)),
+                           ("free_head_out", free_head_out, (1,)),
+                           ("key_counts", key_counts, (B, T)), ("page_counts", page_counts, (B, T))):
+        if t is not None or name in ("key_counts", "page_counts"):
+            _kv_tensor(ctx, name, t, i32, shape)
+    N = page_table.shape[1]
+    _check(lib().kv_block_tables(ctx.handle, _ptr(cached), _ptr(fresh), B, T, P, N,
+                                 _ptr(page_table), page_table.stride(0) if B > 1 else N, n_blocks,
+                                 _ptr(free_list), free_list.numel(), _ptr(free_head),
+                                 _ptr(free_head_out), _ptr(slots), _ptr(key_counts),
+                                 _ptr(page_counts), _stream(stream, slots.device)),
+           "kv_block_tables")
+    return slots, key_counts, page_counts
+
+
+def kv_append(ctx, k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """Rows k, v (bf16 [R][H][D], rows may be strided) into the cache's slots[r] (int32 [R], or any
+    shape of R elements; -1: none), with the scales of the pages they reach."""
+    n_blocks, H, P, D, fmt = _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale)
+    R = slots.numel()
+    _kv_tensor(ctx, "slots", slots, torch.int32, slots.shape)
+    _kv_tensor(ctx, "k", k, _BF16, (R, H, D), contiguous=False)
+    _kv_tensor(ctx, "v", v, _BF16, (R, H, D), contiguous=False)
+    _check(lib().kv_append(ctx.handle, _ptr(k), _ptr(v), _kv_rows("k", k, 1), _kv_rows("v", v, 1),
+                           _ptr(slots), R, H, D, P, n_blocks, fmt, _ptr(k_cache), _ptr(v_cache),
+                           _ptr(k_scale), _ptr(v_scale), _stream(stream, k.device)), "kv_append")
+
+
+def kv_attention(ctx, q, k_cache, v_cache, k_scale, v_scale, page_table, key_counts, out, lse=None,
+                 page_idx=None, scale=None, stream=None):
+    """out (bf16 [B][T][Q][D]) = attention of q (bf16 [B][T][Q][D], rows may be strided) over the
+    first key_counts[b, t] keys of the request: of the pages page_idx[b*T+t] (int32 [B*T][K], -1:
+    none), or of all its pages.  lse: fp32 [B][T][Q] or None; scale: 1/sqrt(D) if None."""
+    n_blocks, H, P, D, fmt = _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale)
+    _kv_tensor(ctx, "q", q, _BF16, (None, None, None, D), contiguous=False)
+    B, T, Q, _ = q.shape
+    _kv_tensor(ctx, "out", out, _BF16, (B, T, Q, D))
+    _kv_tensor(ctx, "page_table", page_table, torch.int32, (B, None), contiguous=False)
+    if page_table.stride(1) != 1 or (B > 1 and page_table.stride(0) < page_table.shape[1]):
+        raise ValueError("page_table's rows must be contiguous")
+    N = page_table.shape[1]
+    if key_counts.numel() != B * T:
+        raise ValueError("key_counts must have B*T elements")
+    _kv_tensor(ctx, "key_counts", key_counts, torch.int32, key_counts.shape)
+    if lse is not None:
+        _kv_tensor(ctx, "lse", lse, torch.float32, (B, T, Q))
+    K = 0
+    if page_idx is not None:
+        _kv_tensor(ctx, "page_idx", page_idx, torch.int32, (B * T, None))
+        K = page_idx.shape[1]
+        if K == 0:
+            raise ValueError("page_idx must have a column")
+    if scale is None:
+        scale = D ** -0.5
+    _check(lib().kv_attention(ctx.handle, _ptr(q), _kv_rows("q", q, 2), _ptr(k_cache),
+                              _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n_blocks, fmt,
+                              _ptr(page_table), page_table.stride(0) if B > 1 else N, N,
+                              _ptr(key_counts), _ptr(page_idx), K, B, T, Q, H, D, P, scale,
+                              _ptr(out), _ptr(lse), _stream(stream, q.device)), "kv_attention")
+    return out, lse

@@ -6,6 +6,7 @@
 // allocated in idx_init; every later call only validates, picks a kernel and
 // launches it on the caller's stream.
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <cuda_runtime.h>
@@ -506,6 +507,134 @@ IDX_API int kmeans_scores(idx_ctx* ctx, const uint16_t* x, const uint16_t* centr
   if (!scores || !aligned16(scores)) return IDX_EINVAL;
   if ((int64_t)M * C > INT32_MAX * 4ll) return IDX_EUNSUPPORTED;
   return kmeans_impl(ctx, x, centroids, M, C, D, nullptr, nullptr, scores, stream);
+}
+
+// ---- 8-bit paged KV cache
+
+// The cache's sizes; rows of all heads and blocks are counted in 31 bits.
+static int check_cache(const void* k_cache, const void* v_cache, const float* k_scale,
+                       const float* v_scale, int n_blocks, int H, int P, int D, int format) {
+  if (!k_cache || !v_cache || !k_scale || !v_scale) return IDX_EINVAL;
+  if (n_blocks <= 0 || H <= 0 || P <= 0 || D <= 0) return IDX_EINVAL;
+  if (format != IDX_KV_E4M3 && format != IDX_KV_INT8) return IDX_EINVAL;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return IDX_EINVAL;
+  if ((reinterpret_cast<uintptr_t>(k_scale) & 3) || (reinterpret_cast<uintptr_t>(v_scale) & 3))
+    return IDX_EINVAL;
+  if ((D % 16) != 0 || D > 256 || H > 65535 || P > 65536) return IDX_EUNSUPPORTED;
+  if ((int64_t)n_blocks * P > INT32_MAX / H) return IDX_EUNSUPPORTED;
+  return IDX_OK;
+}
+
+IDX_API int kv_block_tables(idx_ctx* ctx, const int32_t* cached, const int32_t* fresh, int B, int T,
+                            int P, int N, int32_t* page_table, int64_t ld_pt, int n_blocks,
+                            const int32_t* free_list, int n_free, const int32_t* free_head,
+                            int32_t* free_head_out, int32_t* slots, int32_t* key_counts,
+                            int32_t* page_counts, idx_stream stream) {
+  if (!ctx || !cached || !page_table || !slots || !key_counts || !page_counts) return IDX_EINVAL;
+  if (B <= 0 || T <= 0 || P <= 0 || N <= 0 || n_blocks <= 0 || n_free < 0 || ld_pt < N)
+    return IDX_EINVAL;
+  if (n_free > 0 && !free_list) return IDX_EINVAL;
+  if (free_head_out && free_head_out == free_head) return IDX_EINVAL;
+  if ((int64_t)N * P > INT32_MAX - P || (int64_t)n_blocks * P > INT32_MAX ||
+      (int64_t)B * T > INT32_MAX)
+    return IDX_EUNSUPPORTED;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok()) return IDX_ECUDA;
+  idx::KvTablesArgs a{};
+  a.cached = cached;
+  a.fresh = fresh;
+  a.B = B;
+  a.T = T;
+  a.P = P;
+  a.N = N;
+  a.page_table = page_table;
+  a.ld_pt = ld_pt;
+  a.n_blocks = n_blocks;
+  a.free_list = free_list;
+  a.n_free = n_free;
+  a.free_head = free_head;
+  a.free_head_out = free_head_out;
+  a.slots = slots;
+  a.key_counts = key_counts;
+  a.page_counts = page_counts;
+  a.status = ctx->status;
+  return status_of(idx::launch_kv_tables(a, (cudaStream_t)stream));
+}
+
+IDX_API int kv_append(idx_ctx* ctx, const uint16_t* k, const uint16_t* v, int64_t ldk, int64_t ldv,
+                      const int32_t* slots, int R, int H, int D, int P, int n_blocks, int format,
+                      void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                      idx_stream stream) {
+  if (!ctx || !k || !v || !slots || R <= 0) return IDX_EINVAL;
+  const int rc = check_cache(k_cache, v_cache, k_scale, v_scale, n_blocks, H, P, D, format);
+  if (rc != IDX_OK) return rc;
+  if (!aligned16(k) || !aligned16(v) || (ldk % 8) != 0 || (ldv % 8) != 0) return IDX_EINVAL;
+  if (ldk < (int64_t)H * D || ldv < (int64_t)H * D) return IDX_EINVAL;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok()) return IDX_ECUDA;
+  idx::KvAppendArgs a{};
+  a.k = k;
+  a.v = v;
+  a.ldk = ldk;
+  a.ldv = ldv;
+  a.slots = slots;
+  a.R = R;
+  a.H = H;
+  a.D = D;
+  a.P = P;
+  a.n_blocks = n_blocks;
+  a.format = format;
+  a.k_cache = static_cast<uint8_t*>(k_cache);
+  a.v_cache = static_cast<uint8_t*>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.status = ctx->status;
+  return status_of(idx::launch_kv_append(a, (cudaStream_t)stream));
+}
+
+IDX_API int kv_attention(idx_ctx* ctx, const uint16_t* q, int64_t ldq, const void* k_cache,
+                         const void* v_cache, const float* k_scale, const float* v_scale,
+                         int n_blocks, int format, const int32_t* page_table, int64_t ld_pt, int N,
+                         const int32_t* key_counts, const int32_t* page_idx, int K, int B, int T,
+                         int Q, int H, int D, int P, float scale, uint16_t* out, float* lse,
+                         idx_stream stream) {
+  if (!ctx || !q || !page_table || !key_counts || !out) return IDX_EINVAL;
+  if (B <= 0 || T <= 0 || Q <= 0 || N <= 0 || ld_pt < N) return IDX_EINVAL;
+  if (page_idx ? K <= 0 : K != 0) return IDX_EINVAL;
+  const int rc = check_cache(k_cache, v_cache, k_scale, v_scale, n_blocks, H, P, D, format);
+  if (rc != IDX_OK) return rc;
+  if (Q % H != 0 || !aligned16(q) || !aligned16(out) || (ldq % 8) != 0 || ldq < (int64_t)Q * D)
+    return IDX_EINVAL;
+  if (!std::isfinite(scale)) return IDX_EINVAL;
+  if ((int64_t)N * P > INT32_MAX - P || (int64_t)B * T > INT32_MAX / Q) return IDX_EUNSUPPORTED;
+  DeviceGuard guard(ctx->device);
+  if (!guard.ok()) return IDX_ECUDA;
+  idx::KvAttnArgs a{};
+  a.q = q;
+  a.ldq = ldq;
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.n_blocks = n_blocks;
+  a.format = format;
+  a.page_table = page_table;
+  a.ld_pt = ld_pt;
+  a.N = N;
+  a.key_counts = key_counts;
+  a.page_idx = page_idx;
+  a.K = K;
+  a.B = B;
+  a.T = T;
+  a.Q = Q;
+  a.H = H;
+  a.D = D;
+  a.P = P;
+  a.scale = scale;
+  a.out = out;
+  a.lse = lse;
+  a.status = ctx->status;
+  return status_of(idx::launch_kv_attn(a, (cudaStream_t)stream));
 }
 
 IDX_API int idx_get_status(idx_ctx* ctx, idx_stream stream, int* bits) {

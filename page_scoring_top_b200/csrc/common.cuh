@@ -29,6 +29,7 @@ namespace idx {
 constexpr int kErrLengthClamped = 1;  // a length outside [0, N] was clamped
 constexpr int kErrWaitTimeout = 2;    // a bounded wait gave up (data incomplete)
 constexpr int kErrPageClamped = 4;   // a page-table entry outside the block pool was clamped
+constexpr int kErrNoFreePage = 8;    // the free list ended before every new page had a block
 
 constexpr uint32_t kKeyInvalid = 0u;
 constexpr uint32_t kNegInfBits = 0xFF800000u;

@@ -136,4 +136,62 @@ struct PoolArgs {
 };
 cudaError_t launch_pool(const PoolArgs& a, int num_sms, cudaStream_t stream);
 
+// ---------------------------------------------------------------- 8-bit paged KV cache
+constexpr int kKvE4m3 = 0;  // the ABI's IDX_KV_E4M3
+constexpr int kKvInt8 = 1;  // the ABI's IDX_KV_INT8
+
+struct KvTablesArgs {
+  const int32_t* cached;  // [B]
+  const int32_t* fresh;   // [B], or null (T each)
+  int B, T, P, N;
+  int32_t* page_table;
+  int64_t ld_pt;
+  int n_blocks;
+  const int32_t* free_list;
+  int n_free;
+  const int32_t* free_head;  // or null (0)
+  int32_t* free_head_out;    // or null
+  int32_t* slots;            // [B][T]
+  int32_t* key_counts;       // [B][T]
+  int32_t* page_counts;      // [B][T]
+  int* status;
+};
+cudaError_t launch_kv_tables(const KvTablesArgs& a, cudaStream_t stream);
+
+struct KvAppendArgs {
+  const uint16_t* k;  // bf16, head h of row r at k + r*ldk + h*D
+  const uint16_t* v;
+  int64_t ldk, ldv;
+  const int32_t* slots;  // [R]
+  int R, H, D, P, n_blocks, format;
+  uint8_t* k_cache;  // [n_blocks][H][P][D]
+  uint8_t* v_cache;
+  float* k_scale;  // [n_blocks][H]
+  float* v_scale;
+  int* status;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t stream);
+
+struct KvAttnArgs {
+  const uint16_t* q;  // bf16, head h of row r = b*T + t at q + r*ldq + h*D
+  int64_t ldq;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int n_blocks, format;
+  const int32_t* page_table;
+  int64_t ld_pt;
+  int N;
+  const int32_t* key_counts;  // [B*T]
+  const int32_t* page_idx;    // [B*T][K], or null (all pages)
+  int K;
+  int B, T, Q, H, D, P;
+  float scale;
+  uint16_t* out;  // bf16 [B*T][Q][D]
+  float* lse;     // [B*T][Q], or null
+  int* status;
+};
+cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t stream);
+
 }  // namespace idx
