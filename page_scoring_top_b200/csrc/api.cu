@@ -31,6 +31,8 @@ struct idx_ctx {
   int* status;
   float* scratch;  // fp32 scores for the score-then-select route
   int64_t scratch_elems;
+  float* kv_ws;  // attention over the KV cache: partial results of cut items
+  int32_t* kv_arrive;
 };
 
 namespace {
@@ -242,8 +244,10 @@ IDX_API int idx_init(idx_ctx** out, int device, int max_rows, int max_n, int max
   const size_t o_fidx = carve((size_t)ctx->fused_slots * ctx->fused_stride * 4);
   const size_t o_thr = carve((size_t)max_rows * 8);
   const size_t o_arr = carve((size_t)max_rows * 4);
+  const size_t o_kva = carve((size_t)sms * 4);
   const size_t o_st = carve(16);
   const size_t o_scr = carve((size_t)ctx->scratch_elems * 4);
+  const size_t o_kvw = carve(idx::kv_attn_ws_floats(sms) * 4);
   ctx->ws_bytes = off;
   char* base = nullptr;
   if (cudaMalloc(&base, off) != cudaSuccess) {
@@ -267,6 +271,8 @@ IDX_API int idx_init(idx_ctx** out, int device, int max_rows, int max_n, int max
   ctx->arrive = reinterpret_cast<int32_t*>(base + o_arr);
   ctx->status = reinterpret_cast<int*>(base + o_st);
   ctx->scratch = reinterpret_cast<float*>(base + o_scr);
+  ctx->kv_ws = reinterpret_cast<float*>(base + o_kvw);
+  ctx->kv_arrive = reinterpret_cast<int32_t*>(base + o_kva);
   *out = ctx;
   return IDX_OK;
 }
@@ -633,8 +639,10 @@ IDX_API int kv_attention(idx_ctx* ctx, const uint16_t* q, int64_t ldq, const voi
   a.scale = scale;
   a.out = out;
   a.lse = lse;
+  a.ws = ctx->kv_ws;
+  a.arrive = ctx->kv_arrive;
   a.status = ctx->status;
-  return status_of(idx::launch_kv_attn(a, (cudaStream_t)stream));
+  return status_of(idx::launch_kv_attn(a, ctx->num_sms, (cudaStream_t)stream));
 }
 
 IDX_API int idx_get_status(idx_ctx* ctx, idx_stream stream, int* bits) {

@@ -190,8 +190,11 @@ struct KvAttnArgs {
   float scale;
   uint16_t* out;  // bf16 [B*T][Q][D]
   float* lse;     // [B*T][Q], or null
+  float* ws;        // partial results, kv_attn_ws_floats
+  int32_t* arrive;  // num_sms counters, zero between calls
   int* status;
 };
-cudaError_t launch_kv_attn(const KvAttnArgs& a, cudaStream_t stream);
+size_t kv_attn_ws_floats(int num_sms);
+cudaError_t launch_kv_attn(const KvAttnArgs& a, int num_sms, cudaStream_t stream);
 
 }  // namespace idx

@@ -1,0 +1,1015 @@
+// kv_attn.cuh -- attention over the pages of the 8-bit KV cache, streamed.
+//
+// Row (b, t), query head h, kv head g = h / G (G = Q / H): over the keys i that
+// the row sees,
+//     s_i = scale * (q . k8_i) * ks_i,   out = sum_i softmax(s)_i * v8_i * vs_i,
+// k8, v8 the codes and ks, vs their page's scales.  One pass over the keys with
+// the running maximum and sum of the softmax.
+//
+// The value scale goes into the exponent: with x_i = s_i log2(e) + log2(vs_i)
+// and m the running maximum of x,
+//     p_i = 2^(x_i - m) <= 1,  O += p_i v8_i,  l += p_i / vs_i,
+//     out = O / l,  lse = (m + log2 l) ln 2.
+// So the weights that meet the codes in the tensor cores are at most 1 and their
+// largest is 1 whatever the scales are, and fp16 holds them to 2^-11: e4m3 and
+// int8 codes are exact in fp16, products are exact and sums are fp32.  fp16
+// holds bf16 queries exactly too, after a power of two per row (its inverse
+// goes into the score's factor).  A value scale below 2^-100 counts as 2^-100 in the
+// exponent, and its weights are multiplied by what is left.
+//
+// Work: a row tile is TT tokens of one request (1 with page lists, which differ
+// by token) and up to 16*MT query rows (tokens x heads of one kv head), an item
+// is a row tile and a kv head, a unit is 32 keys of it.  The units of all items
+// are laid end to end and cut evenly over the CTAs (one per SM).  An item that
+// is cut leaves partial results (O, m, l) in the workspace; the last of its
+// CTAs to arrive joins them in the order of the keys.
+//
+// A CTA has one producer warp and eight consumer warps.  The producer looks up
+// 32 units at a time (page list, block table, scales; one per lane), skips
+// those without keys, and has the TMA engine copy the keys and values of each
+// into a ring of stages.  Consumer warp w works on the 16 query rows w % MT of
+// every (8/MT)th stage with an accumulator of its own, so no two warps meet
+// before the item's end; there they join their maxima, sums and accumulators.
+// (Above 128 columns two warps share a stage: each takes the scores, and half
+// of the value columns, which is what its registers hold.)
+// One unit is 32 keys x D codes of K and of V: 8 KB at D = 128.
+//
+// The matrix instruction is the warp-wide m16n8k16: with few query rows a key
+// is used for 2 G flops a byte, far below what the tcgen05 tiles of 128 rows
+// are for, and the codes have to pass through registers to become fp16 anyway:
+// they go from there into the instruction without a second trip through shared
+// memory.  The order of the head dim within a product is free, so a lane takes
+// 16 consecutive codes of a key as four steps' operands; the keys of the
+// product with V come transposed out of ldmatrix as pairs of codes, which one
+// byte permute turns into two operands (even and odd dims).
+#pragma once
+
+#include <cuda.h>
+
+#include "kv.cuh"
+#include "tc.cuh"
+
+namespace idx {
+
+constexpr int kKvConsumers = 8;
+constexpr int kKvThreads = (kKvConsumers + 1) * 32;
+constexpr int kKvUnit = 32;        // keys per unit
+constexpr int kKvMaxStages = 32;
+constexpr int kKvSegs = 64;        // descriptor ring: more than the stages and a group of warps
+constexpr int kKvSmem = 227 * 1024;
+constexpr float kKvMinScale = 7.8886090522101181e-31f;  // 2^-100
+
+// What the host settles for a launch.
+struct KvPlan {
+  int TT;           // tokens per row tile
+  int ntb;          // row tiles per request
+  int GG;           // query heads per item
+  int ng;           // items per kv head
+  int ppt, tpp;     // pages per unit (P < 32) or units per page
+  int pitch;        // rows from page to page in a unit of several pages
+  int box;          // rows of a copy
+  int nstage;
+  float* ws;        // 2 slots per CTA: O [64][256], m [64], l [64]
+  int32_t* arrive;  // one counter per CTA, zero between launches
+};
+constexpr int kKvSlot = 64 * 256 + 128;  // floats of a workspace slot
+
+struct KvSeg {
+  int64_t unit0;    // the item's first unit
+  int nt;           // its units
+  int b, t0, nrow;  // request, first token, query rows (tokens x heads)
+  int h0;           // first query head
+  int first, last;  // whether this segment has the item's first and last unit
+  int max_count;    // keys that the tile's rows see: the most
+};
+
+// Scales of a stage's keys (one entry, or one per key where a unit has several
+// pages): the score's, log2 and inverse of the value's, and what is left of a
+// value scale below 2^-100.  Beside them the position of the (first) key, and
+// per stage its segment, kKvFull and the number of its keys.
+struct KvPage {
+  float ks, lv, iv, rest;
+};
+constexpr int kKvFull = 1;  // every row that sees any key sees all 32
+
+template <int DP, int MT, bool MULTI>
+struct KvLayout {
+  static constexpr int RB = DP < 128 ? DP : 128;      // bytes of a row in a block
+  static constexpr int NB = DP / RB;                  // column blocks
+  static constexpr int NH = DP == 256 ? 2 : 1;        // warps that share a unit's value columns
+  static constexpr int OC = DP / NH;                  // value columns of a warp
+  static constexpr int KG = kKvConsumers / (MT * NH); // groups of warps taking turns
+  static constexpr int kStage = 2 * kKvUnit * DP;     // K then V
+  static constexpr int CM = DP == 256 ? 64 : OC;      // columns of a warp joined at a time
+  static constexpr int kQPitch = DP * 2 + 16;
+  static constexpr int kPages = MULTI ? kKvUnit : 1;  // scale entries: per key or one
+  static constexpr size_t bars = 0;                                    // full, empty
+  static constexpr size_t misc = bars + 2 * kKvMaxStages * 8;          // 64 ints
+  static constexpr size_t seg = misc + 256;
+  static constexpr size_t meta = seg + kKvSegs * sizeof(KvSeg);        // int[4] per stage
+  static constexpr size_t page = meta + kKvMaxStages * 16;
+  static constexpr size_t pos = page + (size_t)kKvMaxStages * kPages * sizeof(KvPage);
+  static constexpr size_t ml = (pos + (size_t)kKvMaxStages * kPages * 4 + 15) & ~(size_t)15;
+  static constexpr size_t rows = ml + kKvConsumers * 16 * 8;           // factor, limit per row
+  static constexpr size_t q = rows + 64 * 12;
+  static constexpr size_t join = q + (size_t)16 * MT * kQPitch;
+  static constexpr size_t ring =
+      (join + (size_t)kKvConsumers * 16 * (CM + 4) * 4 + 1023) & ~(size_t)1023;
+  static constexpr int stages() {
+    const int n = (int)((kKvSmem - 1024 - ring) / kStage);
+    return n < kKvMaxStages ? n : kKvMaxStages;
+  }
+  static constexpr size_t total() { return ring + (size_t)stages() * kStage + 1024; }
+  static_assert(stages() >= KG, "each group of warps needs a stage");
+  static_assert(kKvSegs > kKvMaxStages + KG, "descriptors must outlive their stages");
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                        uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// int8 to fp16: 0x6400 + (code ^ 0x80) is 1024 + 128 + code, exactly.
+__device__ __forceinline__ uint32_t minus_1152(uint32_t w) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0x64806480u));
+  return r;
+}
+
+// Four codes of a word as fp16 pairs: (0, 1), (2, 3), or, ACROSS, (0, 2), (1, 3).
+template <int FMT, bool ACROSS>
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t& x, uint32_t& y) {
+  if (FMT == kKvE4m3) {
+    if (ACROSS) w = __byte_perm(w, 0, 0x3120);
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "mov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(x), "=r"(y)
+        : "r"(w));
+  } else {
+    w ^= 0x80808080u;
+    x = minus_1152(__byte_perm(w, 0x64646464u, ACROSS ? 0x4240 : 0x4140));
+    y = minus_1152(__byte_perm(w, 0x64646464u, ACROSS ? 0x4341 : 0x4342));
+  }
+}
+
+// Units of row tile rt (at least one: a tile without keys still has an output),
+// and the most and fewest keys that its rows with keys see.
+struct KvTile {
+  int nt, max_count, min_count;
+};
+
+__device__ __forceinline__ int kv_count(const KvAttnArgs& a, int64_t r, int& bits) {
+  int c = __ldg(a.key_counts + r);
+  if (c < 0 || c > a.N * a.P) {
+    bits |= kErrLengthClamped;
+    c = c < 0 ? 0 : a.N * a.P;
+  }
+  return c;
+}
+
+__device__ __forceinline__ int kv_units(const KvAttnArgs& a, const KvPlan& pl, int max_count) {
+  int np = (max_count + a.P - 1) / a.P;
+  int64_t nt;
+  if (a.page_idx) {
+    np = np < a.K ? np : a.K;  // a list of distinct pages has no more with keys
+    nt = pl.ppt > 1 ? (np + pl.ppt - 1) / pl.ppt : (int64_t)np * pl.tpp;
+  } else if (pl.ppt > 1) {
+    nt = (np + pl.ppt - 1) / pl.ppt;
+  } else {
+    nt = np ? (int64_t)(np - 1) * pl.tpp + (max_count - (np - 1) * a.P + kKvUnit - 1) / kKvUnit : 0;
+  }
+  return nt < 1 ? 1 : (int)nt;
+}
+
+// One thread's walk over the tile's tokens.
+__device__ __forceinline__ KvTile kv_tile(const KvAttnArgs& a, const KvPlan& pl, int64_t rt,
+                                          int& bits) {
+  const int b = (int)(rt / pl.ntb), t0 = (int)(rt - (int64_t)b * pl.ntb) * pl.TT;
+  const int n = a.T - t0 < pl.TT ? a.T - t0 : pl.TT;
+  KvTile k;
+  k.max_count = 0;
+  k.min_count = INT32_MAX;
+  for (int t = 0; t < n; ++t) {
+    const int c = kv_count(a, (int64_t)b * a.T + t0 + t, bits);
+    k.max_count = c > k.max_count ? c : k.max_count;
+    if (c > 0 && c < k.min_count) k.min_count = c;
+  }
+  k.nt = kv_units(a, pl, k.max_count);
+  return k;
+}
+
+template <int FMT, int DP, int MT, bool MULTI>
+__global__ void __launch_bounds__(kKvThreads, 1)
+    kv_attn_kernel(const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const KvAttnArgs a,
+                   const KvPlan pl) {
+  using L = KvLayout<DP, MT, MULTI>;
+  constexpr int KG = L::KG;
+  constexpr int M = 16 * MT;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::bars);
+  uint64_t* empty = full + kKvMaxStages;
+  int* misc = reinterpret_cast<int*>(smem + L::misc);
+  volatile int* s_abort = misc;        // misc[0]
+  int* s_flag = misc + 2;              // per segment: aborted, last to arrive
+  int64_t* s_where = reinterpret_cast<int64_t*>(misc + 8);  // row tile, units before, both ends
+  long long* s_warp = reinterpret_cast<long long*>(misc + 24);  // 9 warp sums
+  KvSeg* segs = reinterpret_cast<KvSeg*>(smem + L::seg);
+  int* meta = reinterpret_cast<int*>(smem + L::meta);
+  KvPage* pages = reinterpret_cast<KvPage*>(smem + L::page);
+  int* poss = reinterpret_cast<int*>(smem + L::pos);
+  unsigned char* ring = smem + L::ring;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ns = pl.nstage;
+  const int items = a.H * pl.ng;  // items per row tile
+  const int64_t nrt = (int64_t)a.B * pl.ntb;
+  int bits = 0;
+
+  // ---- the split: units before each thread's row tiles, then this CTA's share
+  const int64_t per = (nrt + kKvThreads - 1) / kKvThreads;
+  const int64_t rt0 = tid * per < nrt ? tid * per : nrt;
+  const int64_t rt1 = rt0 + per < nrt ? rt0 + per : nrt;
+  long long mine = 0;
+  for (int64_t rt = rt0; rt < rt1; ++rt) mine += kv_tile(a, pl, rt, bits).nt;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long n = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += n;
+  }
+  if (lane == 31) s_warp[warp] = incl;
+  if (tid < ns) {
+    mbar_init(&full[tid], 1);
+    mbar_init(&empty[tid], MT * L::NH);
+  }
+  if (tid == 0) {
+    *s_abort = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  long long before = 0, total = 0;
+  for (int w = 0; w < kKvThreads / 32; ++w) {
+    if (w < warp) before += s_warp[w];
+    total += s_warp[w];
+  }
+  before += incl - mine;
+  const int64_t W = total * items;
+  // at least a unit for each group of warps, so that a short batch is not cut
+  // into more parts than joining them is worth
+  int64_t nc = W / KG;
+  nc = nc < 1 ? 1 : (nc < (int64_t)gridDim.x ? nc : (int64_t)gridDim.x);
+  if ((int64_t)blockIdx.x >= nc) return;
+  if (tid == 0) {
+    s_where[2] = W;
+    s_where[3] = nc;
+  }
+  const int64_t u_begin = W * blockIdx.x / nc, u_end = W * (blockIdx.x + 1) / nc;
+  {
+    long long base = before * items;
+    if (u_begin < base + mine * items && u_end > base)
+      for (int64_t rt = rt0; rt < rt1; ++rt) {
+        const int64_t n = (int64_t)kv_tile(a, pl, rt, bits).nt * items;
+        if (u_begin >= base && u_begin < base + n) {
+          s_where[0] = rt;
+          s_where[1] = base;
+          s_where[4] = rt * items + (u_begin - base) / (n / items);
+        }
+        if (u_end - 1 >= base && u_end - 1 < base + n)
+          s_where[5] = rt * items + (u_end - 1 - base) / (n / items);
+        base += n;
+      }
+  }
+  __syncthreads();
+  const int nseg = (int)(s_where[5] - s_where[4] + 1);
+
+  if (warp == kKvConsumers) {
+    // =================================================================== producer
+    int64_t rt = s_where[0], base = s_where[1], u = u_begin;
+    int slot = 0, phase = 1;  // a fresh ring is empty
+    int64_t issued = 0;
+    int sidx = 0;
+    bool ok = true;
+    // waits for the stage to be free; false once a wait has expired
+    auto acquire = [&]() {
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[slot], phase, s_abort, a.status));
+      return ok;
+    };
+    auto advance = [&]() {
+      ++issued;
+      if (++slot == ns) {
+        slot = 0;
+        phase ^= 1;
+      }
+    };
+    while (ok && u < u_end) {
+      // the row tile: counts of its tokens, a lane each
+      const int b = (int)(rt / pl.ntb), tk = (int)(rt - (int64_t)b * pl.ntb) * pl.TT;
+      const int ntok = a.T - tk < pl.TT ? a.T - tk : pl.TT;
+      int mx = 0, mn = INT32_MAX;
+      for (int t = lane; t < ntok; t += 32) {
+        const int c = kv_count(a, (int64_t)b * a.T + tk + t, bits);
+        mx = c > mx ? c : mx;
+        if (c > 0 && c < mn) mn = c;
+      }
+      mx = __reduce_max_sync(0xFFFFFFFFu, mx);
+      mn = __reduce_min_sync(0xFFFFFFFFu, mn);
+      const int nt = kv_units(a, pl, mx);
+      const int64_t rt_end = base + (int64_t)nt * items;
+      while (ok && u < u_end && u < rt_end) {
+        const int it = (int)((u - base) / nt);
+        const int t0 = (int)((u - base) - (int64_t)it * nt);
+        const int t1 = nt - t0 < u_end - u ? nt : t0 + (int)(u_end - u);
+        const int g = it / pl.ng, hg = it - g * pl.ng;
+        const int G = a.Q / a.H;
+        const int heads = G - hg * pl.GG < pl.GG ? G - hg * pl.GG : pl.GG;
+        if (lane == 0) {
+          KvSeg& s = segs[sidx % kKvSegs];
+          s.unit0 = base + (int64_t)it * nt;
+          s.nt = nt;
+          s.b = b;
+          s.t0 = tk;
+          s.nrow = ntok * heads;
+          s.h0 = g * G + hg * pl.GG;
+          s.first = t0 == 0;
+          s.last = t1 == nt;
+          s.max_count = mx;
+        }
+        // units of the list: past the expected ones too in the item's last
+        // segment (lists with gaps or repeated pages)
+        const int64_t r = (int64_t)b * a.T + tk;
+        const int np = a.page_idx ? a.K : (mx + a.P - 1) / a.P;
+        int64_t stop = t1;
+        if (mx == 0) stop = t0;
+        else if (a.page_idx && t1 == nt)
+          stop = MULTI ? (np + pl.ppt - 1) / pl.ppt : (int64_t)np * pl.tpp;
+        int emitted = 0;
+        const int tpc = MULTI ? 32 / pl.ppt : 32;  // units per look-up
+        for (int64_t c = t0; c < stop && ok; c += tpc) {
+          int e, sub = 0;
+          bool valid;
+          if (MULTI) {
+            const int64_t e64 = c * pl.ppt + lane;
+            valid = lane < tpc * pl.ppt && e64 < np && c + lane / pl.ppt < stop;
+            e = (int)e64;
+          } else {
+            const int64_t t = c + lane;
+            valid = t < stop;
+            e = (int)(t / pl.tpp);
+            sub = (int)(t - (int64_t)e * pl.tpp) * kKvUnit;
+          }
+          int p = 0, id = 0;
+          if (valid) {
+            p = a.page_idx ? __ldg(a.page_idx + r * a.K + e) : e;
+            if (p < 0 || p >= a.N) {
+              if (p != -1) bits |= kErrPageClamped;
+              valid = false;
+            }
+          }
+          valid = valid && (int64_t)p * a.P + sub < mx;
+          if (valid) {
+            id = __ldg(a.page_table + (int64_t)b * a.ld_pt + p);
+            if (id < 0 || id >= a.n_blocks) {
+              bits |= kErrPageClamped;
+              valid = false;
+            }
+          }
+          KvPage pg{0.f, 0.f, 0.f, 0.f};
+          int pos = INT32_MAX, row = 0, nk = 0;
+          if (valid) {
+            const int64_t cell = (int64_t)id * a.H + g;
+            const float vs = __ldg(a.v_scale + cell);
+            const float v1 = fmaxf(vs, kKvMinScale);
+            pg.ks = __ldg(a.k_scale + cell);
+            // 2^lv must give a power of two back exactly
+            const uint32_t vb = __float_as_uint(v1);
+            pg.lv = (vb & 0x7FFFFFu) ? __log2f(v1) : (float)((int)(vb >> 23) - 127);
+            pg.iv = __fdiv_rn(1.f, v1);
+            pg.rest = vs < kKvMinScale ? vs * (1.f / kKvMinScale) : (vs == vs ? 1.f : vs);
+            pos = p * a.P + sub;
+            row = (int)(cell * a.P) + sub;
+            nk = a.P - sub < kKvUnit ? a.P - sub : kKvUnit;
+            nk = mx - pos < nk ? mx - pos : nk;
+          }
+          const bool whole = valid && nk == (MULTI ? a.P : kKvUnit) && pos + nk <= mn;
+          const uint32_t vmask = __ballot_sync(0xFFFFFFFFu, valid);
+          const uint32_t fmask = __ballot_sync(0xFFFFFFFFu, whole);
+          const int left = (int)(stop - c < tpc ? stop - c : tpc);
+          for (int i = 0; i < left && ok; ++i) {
+            uint32_t who;  // the lanes of this unit
+            if (MULTI)
+              who = (pl.ppt == 32 ? 0xFFFFFFFFu : ((1u << pl.ppt) - 1u)) << (i * pl.ppt);
+            else
+              who = 1u << i;
+            if (!(vmask & who)) continue;
+            if (!acquire()) break;
+            const bool in = (who >> lane) & 1u;
+            const int k = MULTI ? lane - i * pl.ppt : 0;  // page within the unit
+            if (MULTI) {  // lane j writes the entry of key j
+              const int kp = lane / pl.pitch, kr = lane - kp * pl.pitch;
+              const int from = i * pl.ppt + (kp < pl.ppt ? kp : 0);
+              KvPage e;
+              e.ks = __shfl_sync(0xFFFFFFFFu, pg.ks, from);
+              e.lv = __shfl_sync(0xFFFFFFFFu, pg.lv, from);
+              e.iv = __shfl_sync(0xFFFFFFFFu, pg.iv, from);
+              e.rest = __shfl_sync(0xFFFFFFFFu, pg.rest, from);
+              const int ep = __shfl_sync(0xFFFFFFFFu, pos, from);
+              pages[slot * L::kPages + lane] = e;
+              poss[slot * L::kPages + lane] =
+                  kp < pl.ppt && kr < a.P && ((vmask >> from) & 1u) ? ep + kr : INT32_MAX;
+            } else if (in) {
+              pages[slot] = pg;
+              poss[slot] = pos;
+            }
+            const int leader = __ffs(who) - 1;
+            if (lane == leader) {
+              int f = (fmask & who) == who ? kKvFull : 0;
+              if (MULTI && pl.ppt * a.P != kKvUnit) f = 0;
+              meta[slot * 4] = sidx;
+              meta[slot * 4 + 1] = f;
+              meta[slot * 4 + 2] = MULTI ? 0 : nk;
+            }
+            __syncwarp();
+            if (lane == leader)
+              mbar_arrive_expect_tx(&full[slot],
+                                    (uint32_t)__popc(vmask & who) * 2u * L::NB * L::RB *
+                                        (uint32_t)pl.box);
+            __syncwarp();
+            if (in && valid) {
+              unsigned char* dst = ring + (size_t)slot * L::kStage + (MULTI ? k * pl.pitch : 0) * L::RB;
+#pragma unroll
+              for (int cb = 0; cb < L::NB; ++cb) {
+                tma_load_2d(dst + cb * kKvUnit * L::RB, &map_k, cb * L::RB, row, &full[slot]);
+                tma_load_2d(dst + (L::NB + cb) * kKvUnit * L::RB, &map_v, cb * L::RB, row,
+                            &full[slot]);
+              }
+            }
+            __syncwarp();
+            advance();
+            ++emitted;
+          }
+        }
+        if (ok && emitted == 0 && acquire()) {  // a segment without keys still has its stage
+          if (lane == 0) {
+            meta[slot * 4] = sidx;
+            meta[slot * 4 + 1] = 0;
+            meta[slot * 4 + 2] = 0;
+          }
+          if (lane < L::kPages) {
+            pages[slot * L::kPages + lane] = KvPage{0.f, 0.f, 0.f, 0.f};
+            poss[slot * L::kPages + lane] = INT32_MAX;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[slot]);
+          __syncwarp();
+          advance();
+        }
+        ++sidx;
+        u += t1 - t0;
+      }
+      base = rt_end;
+      ++rt;
+    }
+    // a last stage for each group of warps, then the copies in flight
+    for (int i = 0; i < KG && ok; ++i) {
+      if (!acquire()) break;
+      if (lane == 0) {
+        meta[slot * 4] = INT32_MAX;
+        mbar_arrive(&full[slot]);
+      }
+      __syncwarp();
+      advance();
+    }
+    if (lane == 0) {
+      int s = slot, ph = phase;  // walk back over the stages in use
+      for (int64_t i = 0; i < issued && i < ns; ++i) {
+        if (--s < 0) {
+          s = ns - 1;
+          ph ^= 1;
+        }
+        mbar_wait_drain(&full[s], ph ^ 1);
+      }
+    }
+    if (bits) atomicOr(a.status, bits);
+    return;
+  }
+
+  // ===================================================================== consumers
+  const int mt = warp % MT, half = (warp / MT) % L::NH, kg = warp / (MT * L::NH);
+  const int g8 = lane >> 2, c4 = lane & 3;  // row and column quad of a fragment
+  constexpr bool PERM = DP >= 128;
+  // the key of column 2 c4 + e of an 8-key block, and the row that lane group n takes
+  auto key_of = [&](int e) { return PERM ? c4 + 4 * e : 2 * c4 + e; };
+  const int krow = PERM ? (g8 >> 1) + 4 * (g8 & 1) : g8;
+  float* s_m = reinterpret_cast<float*>(smem + L::ml);
+  float* s_l = s_m + kKvConsumers * 16;
+  float* s_qf = reinterpret_cast<float*>(smem + L::rows);
+  int* s_lims = reinterpret_cast<int*>(s_qf + 64);
+  unsigned char* s_q = smem + L::q;
+  float* s_join = reinterpret_cast<float*>(smem + L::join);
+  int slot = kg, phase = 0;
+  bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot], phase, s_abort, a.status));
+  int cur = ok ? meta[slot * 4] : INT32_MAX;
+
+  for (int s = 0; s < nseg; ++s) {
+    // On an expired wait (cur is then "past every segment") the descriptors may
+    // be missing: the warps still meet at every barrier, and write nothing.
+    const KvSeg& sg = segs[s % kKvSegs];
+    int* s_lim = s_lims + (s & 1) * 64;  // still read when the next item's is written
+    // ---- queries: a warp per row, normalised to a power of two, as fp16
+    {
+      const int G = a.Q / a.H;
+      const int hh = sg.h0 % G;
+      const int nh = G - hh < pl.GG ? G - hh : pl.GG;  // heads of this item
+#pragma unroll
+      for (int i = 0; i < M / kKvConsumers; ++i) {
+        const int m = warp + i * kKvConsumers;
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        int lim = 0;
+        if (ok && m < sg.nrow) {
+          const int tt = m / nh;
+          const int64_t r = (int64_t)sg.b * a.T + sg.t0 + tt;
+          int dummy = 0;
+          lim = kv_count(a, r, dummy);
+          if (lane * 8 < a.D)
+            v = __ldg(reinterpret_cast<const uint4*>(a.q + r * a.ldq +
+                                                     (int64_t)(sg.h0 + m - tt * nh) * a.D + lane * 8));
+        }
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+          top = lo < 0x7F80u && lo > top ? lo : top;
+          top = hi < 0x7F80u && hi > top ? hi : top;
+        }
+        int e = (int)(__reduce_max_sync(0xFFFFFFFFu, top) >> 7);  // exponent field of the largest
+        e = e < 1 ? 1 : (e > 252 ? 252 : e);
+        const float f = __int_as_float((254 - e) << 23);  // 2^(127 - e)
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+        if (lane * 8 < DP)
+          *reinterpret_cast<uint4*>(s_q + m * L::kQPitch + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
+        if (lane == 0) {
+          s_qf[m] = a.scale * 1.44269504088896340736f * __int_as_float(e << 23);
+          s_lim[m] = lim;
+        }
+      }
+    }
+    group_sync(kKvConsumers * 32);
+    const int row0 = mt * 16 + g8;
+    const float qf0 = s_qf[row0], qf1 = s_qf[row0 + 8];
+    const int lim0 = s_lim[row0], lim1 = s_lim[row0 + 8];
+    constexpr bool QREG = DP <= 128;
+    constexpr int NQ = QREG ? DP / 16 : 1;
+    uint32_t qa[NQ][4];
+    // operand of k step i (16 dims) of 64-dim half h: dims 64 h + 16 c4 + 4 i ..
+    auto load_q2 = [&](int hi2, uint32_t (&x)[4], uint32_t (&y)[4]) {
+      // two steps at once: hi2 = (64-dim half) * 2 + pair
+      const unsigned char* p0 =
+          s_q + row0 * L::kQPitch + (hi2 >> 1) * 128 + c4 * 32 + (hi2 & 1) * 16;
+      const uint4 u0 = *reinterpret_cast<const uint4*>(p0);
+      const uint4 u1 = *reinterpret_cast<const uint4*>(p0 + 8 * L::kQPitch);
+      x[0] = u0.x; x[2] = u0.y; y[0] = u0.z; y[2] = u0.w;
+      x[1] = u1.x; x[3] = u1.y; y[1] = u1.z; y[3] = u1.w;
+    };
+    if (QREG) {
+#pragma unroll
+      for (int i = 0; i < NQ / 2; ++i) load_q2(i, qa[2 * i], qa[2 * i + 1]);
+    }
+    float oacc[L::OC / 16][2][4];
+#pragma unroll
+    for (int j = 0; j < L::OC / 16; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) oacc[j][e][k] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+    while (cur == s) {
+      const unsigned char* kb_ = ring + (size_t)slot * L::kStage;
+      const uint32_t vb_ = smem_u32(kb_) + kKvUnit * DP;
+      const bool is_full = (meta[slot * 4 + 1] & kKvFull) != 0;
+      const int nk = meta[slot * 4 + 2];
+      // ---- scores
+      float sc[4][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) sc[k][x] = 0.f;
+#pragma unroll
+      for (int h = 0; h < DP / 64; ++h) {
+        uint32_t q4[4][4];
+        if (!QREG) {
+          load_q2(2 * h, q4[0], q4[1]);
+          load_q2(2 * h + 1, q4[2], q4[3]);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row = k * 8 + krow;
+          const int chunk = DP == 64 ? (c4 ^ ((row >> 1) & 3)) : (((h & 1) * 4 + c4) ^ (row & 7));
+          const uint4 w = *reinterpret_cast<const uint4*>(
+              kb_ + (DP == 256 ? (h >> 1) * kKvUnit * 128 : 0) + row * L::RB + chunk * 16);
+          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t b0, b1;
+            codes4<FMT, false>(ww[i], b0, b1);
+            if (QREG) mma_f16(sc[k], qa[QREG ? h * 4 + i : 0], b0, b1);
+            else mma_f16(sc[k], q4[i], b0, b1);
+          }
+        }
+      }
+      // ---- scales, masks, running maximum
+      float iv[MULTI ? 8 : 1], rest[MULTI ? 8 : 1];
+      int pos[MULTI ? 8 : 1];
+      bool tiny = false;
+      if (MULTI) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = (i >> 1) * 8 + key_of(i & 1);
+          const KvPage pg = pages[slot * L::kPages + (MULTI ? j : 0)];
+          iv[MULTI ? i : 0] = pg.iv;
+          rest[MULTI ? i : 0] = pg.rest;
+          pos[MULTI ? i : 0] = poss[slot * L::kPages + (MULTI ? j : 0)];
+          float(&x)[4] = sc[i >> 1];
+          x[i & 1] = fmaf(x[i & 1], pg.ks * qf0, pg.lv);
+          x[2 + (i & 1)] = fmaf(x[2 + (i & 1)], pg.ks * qf1, pg.lv);
+        }
+        tiny = true;
+      } else {
+        const KvPage pg = pages[slot];
+        pos[0] = poss[slot];
+        iv[0] = pg.iv;
+        rest[0] = pg.rest;
+        tiny = pg.rest != 1.f;
+        const float f0 = pg.ks * qf0, f1 = pg.ks * qf1;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          sc[k][0] = fmaf(sc[k][0], f0, pg.lv);
+          sc[k][1] = fmaf(sc[k][1], f0, pg.lv);
+          sc[k][2] = fmaf(sc[k][2], f1, pg.lv);
+          sc[k][3] = fmaf(sc[k][3], f1, pg.lv);
+        }
+      }
+      if (!is_full) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = (i >> 1) * 8 + key_of(i & 1);
+          const int ps = MULTI ? pos[MULTI ? i : 0] : (j < nk ? pos[0] + j : INT32_MAX);
+          if (ps >= lim0) sc[i >> 1][i & 1] = -INFINITY;
+          if (ps >= lim1) sc[i >> 1][2 + (i & 1)] = -INFINITY;
+        }
+      }
+      float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+      x0 = fmaxf(x0, fmaxf(fmaxf(sc[2][0], sc[2][1]), fmaxf(sc[3][0], sc[3][1])));
+      x1 = fmaxf(x1, fmaxf(fmaxf(sc[2][2], sc[2][3]), fmaxf(sc[3][2], sc[3][3])));
+      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
+      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
+      if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
+        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+        const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
+        const float f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
+        m0 = n0;
+        m1 = n1;
+        l0 *= f0;
+        l1 *= f1;
+#pragma unroll
+        for (int j = 0; j < L::OC / 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            oacc[j][e][0] *= f0;
+            oacc[j][e][1] *= f0;
+            oacc[j][e][2] *= f1;
+            oacc[j][e][3] *= f1;
+          }
+      }
+      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
+      uint32_t pa[2][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float p[4];
+        p[0] = ex2(sc[k][0] - z0);
+        p[1] = ex2(sc[k][1] - z0);
+        p[2] = ex2(sc[k][2] - z1);
+        p[3] = ex2(sc[k][3] - z1);
+        l0 = fmaf(p[0], iv[MULTI ? 2 * k : 0], l0);
+        l0 = fmaf(p[1], iv[MULTI ? 2 * k + 1 : 0], l0);
+        l1 = fmaf(p[2], iv[MULTI ? 2 * k : 0], l1);
+        l1 = fmaf(p[3], iv[MULTI ? 2 * k + 1 : 0], l1);
+        if (tiny) {
+          p[0] *= rest[MULTI ? 2 * k : 0];
+          p[1] *= rest[MULTI ? 2 * k + 1 : 0];
+          p[2] *= rest[MULTI ? 2 * k : 0];
+          p[3] *= rest[MULTI ? 2 * k + 1 : 0];
+        }
+        pa[k >> 1][(k & 1) * 2] = pack_f16(p[0], p[1]);
+        pa[k >> 1][(k & 1) * 2 + 1] = pack_f16(p[2], p[3]);
+      }
+      // ---- O += P V
+      uint32_t keep[4];  // bytes of this lane's two keys that some row sees
+      if (!is_full) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          keep[k] = 0;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int j = k * 8 + key_of(e);
+            const int ps = MULTI ? pos[MULTI ? 2 * k + e : 0] : (j < nk ? pos[0] + j : INT32_MAX);
+            if (ps < sg.max_count) keep[k] |= 0xFFFFu << (16 * e);
+          }
+        }
+      }
+      const int vrow = PERM ? ((lane & 7) >> 1) + 4 * (lane & 1) : (lane & 7);
+      // lane i of a group of 8 gives the address of matrix row i: the key of
+      // the score's column i
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) {
+        const int row = kk * 16 + ((lane >> 3) & 1) * 8 + vrow;
+#pragma unroll
+        for (int j2 = 0; j2 < L::OC / 32; ++j2) {
+          const int ch = j2 * 2 + (lane >> 4);
+          const int chunk = DP == 64 ? (ch ^ ((row >> 1) & 3)) : ((ch & 7) ^ (row & 7));
+          uint32_t r[4];
+          ldsm4_t(r, vb_ + half * (kKvUnit * 128) + row * L::RB + chunk * 16);
+          if (!is_full) {
+            r[0] &= keep[2 * kk];
+            r[1] &= keep[2 * kk + 1];
+            r[2] &= keep[2 * kk];
+            r[3] &= keep[2 * kk + 1];
+          }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            uint32_t e0, o0, e1, o1;
+            codes4<FMT, true>(r[2 * x], e0, o0);
+            codes4<FMT, true>(r[2 * x + 1], e1, o1);
+            if (FMT == kKvE4m3 && !is_full && pl.TT > 1) {
+              // Rows of several tokens, and keys that not all of them see: a
+              // NaN among those must reach the rows that do, and only them
+              // (zero weights do not stop it).
+              auto bad = [](uint32_t w) {
+                return (((w & 0x7FFFu) > 0x7C00u) ? 0xFFFFu : 0u) |
+                       (((w & 0x7FFF0000u) > 0x7C000000u) ? 0xFFFF0000u : 0u);
+              };
+              const uint32_t be0 = bad(e0), be1 = bad(e1), bo0 = bad(o0), bo1 = bad(o1);
+              if (__any_sync(0xFFFFFFFFu, (be0 | be1 | bo0 | bo1) != 0)) {
+                uint32_t see[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {  // 1 where the row sees the key
+                  const int k = 2 * kk + (y >> 1);
+                  const int lim = (y & 1) ? lim1 : lim0;
+                  see[y] = 0;
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const int jj = k * 8 + key_of(e);
+                    const int ps =
+                        MULTI ? pos[MULTI ? 2 * k + e : 0] : (jj < nk ? pos[0] + jj : INT32_MAX);
+                    if (ps < lim) see[y] |= 0x3C00u << (16 * e);
+                  }
+                }
+                float te[4] = {0.f, 0.f, 0.f, 0.f}, to[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(te, see, be0 & 0x3C003C00u, be1 & 0x3C003C00u);
+                mma_f16(to, see, bo0 & 0x3C003C00u, bo1 & 0x3C003C00u);
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                  if (te[y] > 0.f) oacc[j2 * 2 + x][0][y] = __int_as_float(0x7FC00000);
+                  if (to[y] > 0.f) oacc[j2 * 2 + x][1][y] = __int_as_float(0x7FC00000);
+                }
+                e0 &= ~be0;
+                e1 &= ~be1;
+                o0 &= ~bo0;
+                o1 &= ~bo1;
+              }
+            }
+            mma_f16(oacc[j2 * 2 + x][0], pa[kk], e0, e1);
+            mma_f16(oacc[j2 * 2 + x][1], pa[kk], o0, o1);
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[slot]);
+      slot += KG;
+      if (slot >= ns) {
+        slot -= ns;
+        phase ^= 1;
+      }
+      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot], phase, s_abort, a.status));
+      cur = ok ? meta[slot * 4] : INT32_MAX;
+    }
+
+    // ---- the item's end: join the groups of warps
+    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
+    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
+    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2);
+    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
+    if (c4 == 0) {
+      s_m[warp * 16 + g8] = m0;
+      s_m[warp * 16 + g8 + 8] = m1;
+      s_l[warp * 16 + g8] = l0;
+      s_l[warp * 16 + g8 + 8] = l1;
+    }
+    if (tid == 0) s_flag[0] = *s_abort;
+    group_sync(kKvConsumers * 32);
+    const bool aborted = s_flag[0] != 0;
+    float mm0 = -INFINITY, mm1 = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < KG; ++k) {
+      mm0 = fmaxf(mm0, s_m[(k * L::NH * MT + mt) * 16 + g8]);
+      mm1 = fmaxf(mm1, s_m[(k * L::NH * MT + mt) * 16 + g8 + 8]);
+    }
+    const float f0 = m0 == -INFINITY ? (l0 == l0 ? 0.f : l0) : ex2(m0 - mm0);
+    const float f1 = m1 == -INFINITY ? (l1 == l1 ? 0.f : l1) : ex2(m1 - mm1);
+    const int part = sg.first && sg.last ? 0 : 1;  // the item is in several CTAs
+    float* wslot = pl.ws + (int64_t)(2 * blockIdx.x + (sg.first ? 1 : 0)) * kKvSlot;
+    const int G = a.Q / a.H;
+    const int nh = G - sg.h0 % G < pl.GG ? G - sg.h0 % G : pl.GG;
+    constexpr int CM = L::CM, JP = CM + 4;
+    constexpr int CPR = CM / 8;  // 8-column pieces of a row
+#pragma unroll
+    for (int cb = 0; cb < L::OC / CM; ++cb) {
+      if (cb) group_sync(kKvConsumers * 32);
+#pragma unroll
+      for (int j = 0; j < CM / 16; ++j) {
+        float* d = s_join + (warp * 16 + g8) * JP + j * 16 + c4 * 4;
+        auto& o = oacc[cb * (CM / 16) + j];
+        *reinterpret_cast<float4*>(d) =
+            make_float4(o[0][0] * f0, o[1][0] * f0, o[0][1] * f0, o[1][1] * f0);
+        *reinterpret_cast<float4*>(d + 8 * JP) =
+            make_float4(o[0][2] * f1, o[1][2] * f1, o[0][3] * f1, o[1][3] * f1);
+      }
+      group_sync(kKvConsumers * 32);
+      for (int i = tid; i < M * L::NH * CPR; i += kKvConsumers * 32) {
+        const int row = i / (L::NH * CPR), hf = (i / CPR) % L::NH, col = (i % CPR) * 8;
+        const int oc = hf * L::OC + cb * CM + col;  // the output column
+        if (aborted || row >= sg.nrow || oc >= a.D) continue;
+        const int rm = row & 15, rt16 = row >> 4;
+        float m = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) m = fmaxf(m, s_m[(k * L::NH * MT + rt16) * 16 + rm]);
+        float l = 0.f, o[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) o[x] = 0.f;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          const int w = (k * L::NH + hf) * MT + rt16;
+          const float mw = s_m[w * 16 + rm], lw = s_l[w * 16 + rm];
+          l += mw == -INFINITY ? (lw == lw ? 0.f : lw) : lw * ex2(mw - m);
+          const float4 u0 = *reinterpret_cast<const float4*>(s_join + (w * 16 + rm) * JP + col);
+          const float4 u1 = *reinterpret_cast<const float4*>(s_join + (w * 16 + rm) * JP + col + 4);
+          o[0] += u0.x; o[1] += u0.y; o[2] += u0.z; o[3] += u0.w;
+          o[4] += u1.x; o[5] += u1.y; o[6] += u1.z; o[7] += u1.w;
+        }
+        const bool none = s_lim[row] == 0;
+        if (part) {
+          float* d = wslot + row * 256 + oc;
+          *reinterpret_cast<float4*>(d) = make_float4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<float4*>(d + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          if (oc == 0) {
+            wslot[64 * 256 + row] = m;
+            wslot[64 * 256 + 64 + row] = none ? 0.f : l;
+          }
+        } else {
+          const int tt = row / nh;
+          const int64_t rq = ((int64_t)sg.b * a.T + sg.t0 + tt) * a.Q + sg.h0 + row - tt * nh;
+          const bool zero = none || l == 0.f;
+          uint32_t p[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            p[x] = zero ? 0u
+                        : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(o[2 * x], l))) |
+                              ((uint32_t)__bfloat16_as_ushort(
+                                   __float2bfloat16_rn(__fdiv_rn(o[2 * x + 1], l)))
+                               << 16);
+          *reinterpret_cast<uint4*>(a.out + rq * a.D + oc) =
+              make_uint4(p[0], p[1], p[2], p[3]);
+          if (oc == 0 && a.lse)
+            a.lse[rq] = zero ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+        }
+      }
+    }
+    if (part && !aborted) {
+      // the item's CTAs: c0 holds its first unit, c1 its last
+      const int64_t W = s_where[2], nc = s_where[3];
+      const int64_t c0 = ((sg.unit0 + 1) * nc + W - 1) / W - 1;
+      const int64_t c1 = ((sg.unit0 + sg.nt) * nc + W - 1) / W - 1;
+      const int np = (int)(c1 - c0) + 1;
+      __threadfence();
+      group_sync(kKvConsumers * 32);
+      if (tid == 0) {
+        const int before_ = atomicAdd(pl.arrive + c0, 1);
+        s_flag[1] = before_ == np - 1;
+        if (before_ == np - 1) pl.arrive[c0] = 0;
+      }
+      group_sync(kKvConsumers * 32);
+      if (s_flag[1]) {
+        __threadfence();
+        // part 0 is in the second slot of its CTA, the others in the first of theirs
+        auto at = [&](int i) {
+          return pl.ws + (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kKvSlot;
+        };
+        const int cpr = a.D / 8;
+        for (int i = tid; i < sg.nrow * cpr; i += kKvConsumers * 32) {
+          const int row = i / cpr, col = (i - row * cpr) * 8;
+          float m = -INFINITY;
+          for (int k = 0; k < np; ++k) m = fmaxf(m, __ldcg(at(k) + 64 * 256 + row));
+          float l = 0.f, o[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) o[x] = 0.f;
+          for (int k = 0; k < np; ++k) {
+            const float* p = at(k);
+            const float mk = __ldcg(p + 64 * 256 + row), lk = __ldcg(p + 64 * 256 + 64 + row);
+            const float f = mk == -INFINITY ? (lk == lk ? 0.f : lk) : ex2(mk - m);
+            const float4 u0 = __ldcg(reinterpret_cast<const float4*>(p + row * 256 + col));
+            const float4 u1 = __ldcg(reinterpret_cast<const float4*>(p + row * 256 + col + 4));
+            l = fmaf(lk, f, l);
+            o[0] = fmaf(u0.x, f, o[0]); o[1] = fmaf(u0.y, f, o[1]);
+            o[2] = fmaf(u0.z, f, o[2]); o[3] = fmaf(u0.w, f, o[3]);
+            o[4] = fmaf(u1.x, f, o[4]); o[5] = fmaf(u1.y, f, o[5]);
+            o[6] = fmaf(u1.z, f, o[6]); o[7] = fmaf(u1.w, f, o[7]);
+          }
+          const int tt = row / nh;
+          const int64_t rq = ((int64_t)sg.b * a.T + sg.t0 + tt) * a.Q + sg.h0 + row - tt * nh;
+          const bool zero = l == 0.f;
+          uint32_t p[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            p[x] = zero ? 0u
+                        : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(o[2 * x], l))) |
+                              ((uint32_t)__bfloat16_as_ushort(
+                                   __float2bfloat16_rn(__fdiv_rn(o[2 * x + 1], l)))
+                               << 16);
+          *reinterpret_cast<uint4*>(a.out + rq * a.D + col) = make_uint4(p[0], p[1], p[2], p[3]);
+          if (col == 0 && a.lse)
+            a.lse[rq] = zero ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+        }
+      }
+    }
+  }
+}
+
+template <int DP>
+cudaError_t launch_kv_attn_dp(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& a,
+                              KvPlan pl, int mt, int grid, cudaStream_t stream);
+
+#ifdef IDX_KV_ATTN_DP
+template <int FMT, int DP, int MT, bool MULTI>
+static cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& a,
+                              KvPlan& pl, int grid, cudaStream_t stream) {
+  using L = KvLayout<DP, MT, MULTI>;
+  pl.nstage = L::stages();
+  const size_t smem = L::total();
+  auto kern = kv_attn_kernel<FMT, DP, MT, MULTI>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kKvThreads, smem, stream>>>(mk, mv, a, pl);
+  return cudaGetLastError();
+}
+
+template <>
+cudaError_t launch_kv_attn_dp<IDX_KV_ATTN_DP>(const CUtensorMap& mk, const CUtensorMap& mv,
+                                              const KvAttnArgs& a, KvPlan pl, int mt, int grid,
+                                              cudaStream_t stream) {
+  constexpr int DP = IDX_KV_ATTN_DP;
+  const bool multi = pl.ppt > 1;
+#define IDX_KV_GO(F, M)                                                            \
+  (multi ? launch_one<F, DP, M, true>(mk, mv, a, pl, grid, stream)                 \
+         : launch_one<F, DP, M, false>(mk, mv, a, pl, grid, stream))
+  if (a.format == kKvE4m3)
+    return mt == 1 ? IDX_KV_GO(kKvE4m3, 1) : mt == 2 ? IDX_KV_GO(kKvE4m3, 2) : IDX_KV_GO(kKvE4m3, 4);
+  return mt == 1 ? IDX_KV_GO(kKvInt8, 1) : mt == 2 ? IDX_KV_GO(kKvInt8, 2) : IDX_KV_GO(kKvInt8, 4);
+#undef IDX_KV_GO
+}
+#endif
+
+}  // namespace idx
