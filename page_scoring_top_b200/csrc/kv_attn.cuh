@@ -24,10 +24,12 @@
 // is cut leaves partial results (O, m, l) in the workspace; the last of its
 // CTAs to arrive joins them in the order of the keys.
 //
-// A CTA has one producer warp and eight consumer warps.  The producer looks up
+// A CTA has four producer warps and eight consumer warps.  A producer looks up
 // 32 units at a time (page list, block table, scales; one per lane), skips
 // those without keys, and has the TMA engine copy the keys and values of each
-// into a ring of stages.  Consumer warp w works on the 16 query rows w % MT of
+// into a ring of stages.  The producers take the look-ups in turns, so that
+// four chains of dependent loads are under way; they fill the stages in order,
+// each passing the number used so far to the next.  Consumer warp w works on the 16 query rows w % MT of
 // every (8/MT)th stage with an accumulator of its own, so no two warps meet
 // before the item's end; there they join their maxima, sums and accumulators.
 // (Above 128 columns two warps share a stage: each takes the scores, and half
@@ -52,9 +54,11 @@
 namespace idx {
 
 constexpr int kKvConsumers = 8;
-constexpr int kKvThreads = (kKvConsumers + 1) * 32;
+constexpr int kKvProducers = 4;
+constexpr int kKvThreads = (kKvConsumers + kKvProducers) * 32;
 constexpr int kKvUnit = 32;        // keys per unit
 constexpr int kKvMaxStages = 32;
+constexpr int kKvBatch = 4;        // units the producer issues at once
 constexpr int kKvSegs = 64;        // descriptor ring: more than the stages and a group of warps
 constexpr int kKvSmem = 227 * 1024;
 constexpr float kKvMinScale = 7.8886090522101181e-31f;  // 2^-100
@@ -240,7 +244,9 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   volatile int* s_abort = misc;        // misc[0]
   int* s_flag = misc + 2;              // per segment: aborted, last to arrive
   int64_t* s_where = reinterpret_cast<int64_t*>(misc + 8);  // row tile, units before, both ends
-  long long* s_warp = reinterpret_cast<long long*>(misc + 24);  // 9 warp sums
+  long long* s_warp = reinterpret_cast<long long*>(misc + 24);  // warp sums
+  volatile unsigned long long* s_tot =  // per look-up: its number, stages before it
+      reinterpret_cast<volatile unsigned long long*>(misc + 48);
   KvSeg* segs = reinterpret_cast<KvSeg*>(smem + L::seg);
   int* meta = reinterpret_cast<int*>(smem + L::meta);
   KvPage* pages = reinterpret_cast<KvPage*>(smem + L::page);
@@ -268,11 +274,15 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   if (tid < ns) {
     mbar_init(&full[tid], 1);
     mbar_init(&empty[tid], MT * L::NH);
-  }
-  if (tid == 0) {
-    *s_abort = 0;
     fence_mbar_init();
   }
+  if (tid == 0) *s_abort = 0;
+  if (tid < kKvProducers) s_tot[tid] = tid ? ~0ull : 0ull;
+  if (MULTI)  // rows between and behind a unit's pages hold no key
+    for (int i = tid; i < kKvMaxStages * L::kPages; i += kKvThreads) {
+      pages[i] = KvPage{0.f, 0.f, 0.f, 0.f};
+      poss[i] = INT32_MAX;
+    }
   __syncthreads();
   long long before = 0, total = 0;
   for (int w = 0; w < kKvThreads / 32; ++w) {
@@ -309,24 +319,36 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   __syncthreads();
   const int nseg = (int)(s_where[5] - s_where[4] + 1);
 
-  if (warp == kKvConsumers) {
-    // =================================================================== producer
+  if (warp >= kKvConsumers) {
+    // =================================================================== producers
+    const int pw = warp - kKvConsumers;
     int64_t rt = s_where[0], base = s_where[1], u = u_begin;
-    int slot = 0, phase = 1;  // a fresh ring is empty
-    int64_t issued = 0;
+    uint32_t look = 0;            // look-ups so far, of all producers
     int sidx = 0;
     bool ok = true;
-    // waits for the stage to be free; false once a wait has expired
-    auto acquire = [&]() {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[slot], phase, s_abort, a.status));
-      return ok;
-    };
-    auto advance = [&]() {
-      ++issued;
-      if (++slot == ns) {
-        slot = 0;
-        phase ^= 1;
+    uint64_t *last0 = nullptr, *last1 = nullptr;  // this lane's latest copies
+    int par0 = 0, par1 = 0;
+    // The stages used before look-up `look`, once its predecessor has filled its own.
+    auto stages_before = [&](uint32_t& n) {
+      for (uint32_t it = 0; it < kMaxWaitIters; ++it) {
+        const unsigned long long v = s_tot[look % kKvProducers];
+        if ((uint32_t)(v >> 32) == look) {
+          __threadfence_block();
+          n = (uint32_t)v;
+          return true;
+        }
+        if (*s_abort) return false;
+        __nanosleep(100);  // leaves the issue slots to the consumers
       }
+      *s_abort = 1;
+      atomicOr(a.status, kErrWaitTimeout);
+      return false;
+    };
+    auto tell = [&](uint32_t n) {  // whole warp: its shared-memory writes come first
+      __threadfence_block();
+      __syncwarp();
+      if (lane == 0)
+        s_tot[(look + 1) % kKvProducers] = ((unsigned long long)(look + 1) << 32) | n;
     };
     while (ok && u < u_end) {
       // the row tile: counts of its tokens, a lane each
@@ -349,18 +371,6 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         const int g = it / pl.ng, hg = it - g * pl.ng;
         const int G = a.Q / a.H;
         const int heads = G - hg * pl.GG < pl.GG ? G - hg * pl.GG : pl.GG;
-        if (lane == 0) {
-          KvSeg& s = segs[sidx % kKvSegs];
-          s.unit0 = base + (int64_t)it * nt;
-          s.nt = nt;
-          s.b = b;
-          s.t0 = tk;
-          s.nrow = ntok * heads;
-          s.h0 = g * G + hg * pl.GG;
-          s.first = t0 == 0;
-          s.last = t1 == nt;
-          s.max_count = mx;
-        }
         // units of the list: past the expected ones too in the item's last
         // segment (lists with gaps or repeated pages)
         const int64_t r = (int64_t)b * a.T + tk;
@@ -369,9 +379,14 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         if (mx == 0) stop = t0;
         else if (a.page_idx && t1 == nt)
           stop = MULTI ? (np + pl.ppt - 1) / pl.ppt : (int64_t)np * pl.tpp;
-        int emitted = 0;
         const int tpc = MULTI ? 32 / pl.ppt : 32;  // units per look-up
-        for (int64_t c = t0; c < stop && ok; c += tpc) {
+        int64_t c = t0;
+        do {  // a segment without units has a look-up too: its stage without keys
+          if (look % kKvProducers != (uint32_t)pw) {
+            ++look;
+            c += tpc;
+            continue;
+          }
           int e, sub = 0;
           bool valid;
           if (MULTI) {
@@ -420,101 +435,137 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           const bool whole = valid && nk == (MULTI ? a.P : kKvUnit) && pos + nk <= mn;
           const uint32_t vmask = __ballot_sync(0xFFFFFFFFu, valid);
           const uint32_t fmask = __ballot_sync(0xFFFFFFFFu, whole);
-          const int left = (int)(stop - c < tpc ? stop - c : tpc);
-          for (int i = 0; i < left && ok; ++i) {
-            uint32_t who;  // the lanes of this unit
-            if (MULTI)
-              who = (pl.ppt == 32 ? 0xFFFFFFFFu : ((1u << pl.ppt) - 1u)) << (i * pl.ppt);
-            else
-              who = 1u << i;
-            if (!(vmask & who)) continue;
-            if (!acquire()) break;
-            const bool in = (who >> lane) & 1u;
-            const int k = MULTI ? lane - i * pl.ppt : 0;  // page within the unit
-            if (MULTI) {  // lane j writes the entry of key j
-              const int kp = lane / pl.pitch, kr = lane - kp * pl.pitch;
-              const int from = i * pl.ppt + (kp < pl.ppt ? kp : 0);
-              KvPage e;
-              e.ks = __shfl_sync(0xFFFFFFFFu, pg.ks, from);
-              e.lv = __shfl_sync(0xFFFFFFFFu, pg.lv, from);
-              e.iv = __shfl_sync(0xFFFFFFFFu, pg.iv, from);
-              e.rest = __shfl_sync(0xFFFFFFFFu, pg.rest, from);
-              const int ep = __shfl_sync(0xFFFFFFFFu, pos, from);
-              pages[slot * L::kPages + lane] = e;
-              poss[slot * L::kPages + lane] =
-                  kp < pl.ppt && kr < a.P && ((vmask >> from) & 1u) ? ep + kr : INT32_MAX;
-            } else if (in) {
-              pages[slot] = pg;
-              poss[slot] = pos;
+          // this lane's unit: its lanes, its first lane, its place among the
+          // look-up's units with keys
+          const int unit = MULTI ? lane / pl.ppt : lane;
+          const uint32_t who =
+              MULTI ? (pl.ppt == 32 ? 0xFFFFFFFFu : ((1u << pl.ppt) - 1u) << ((unit * pl.ppt) & 31))
+                    : 1u << lane;
+          const bool busy = (vmask & who) != 0 && unit < tpc;
+          const bool leads = busy && (!MULTI || lane == unit * pl.ppt);
+          const uint32_t lead = __ballot_sync(0xFFFFFFFFu, leads);
+          const int found = __popc(lead);
+          const bool none = found == 0 && c == t0;
+          const int n = none ? 1 : found;
+          uint32_t used = 0;
+          ok = __all_sync(0xFFFFFFFFu, stages_before(used));
+          if (!ok) break;
+          if (c == t0 && lane == 0) {
+            KvSeg& s = segs[sidx % kKvSegs];
+            s.unit0 = base + (int64_t)it * nt;
+            s.nt = nt;
+            s.b = b;
+            s.t0 = tk;
+            s.nrow = ntok * heads;
+            s.h0 = g * G + hg * pl.GG;
+            s.first = t0 == 0;
+            s.last = t1 == nt;
+            s.max_count = mx;
+          }
+          int slot = (int)(used % (uint32_t)ns), phase = (int)((used / (uint32_t)ns) & 1) ^ 1;
+          const int place = __popc(lead & ((MULTI ? 1u << ((unit * pl.ppt) & 31) : 1u << lane) - 1u));
+          int my = slot + place, my_phase = phase;  // the stage and its phase
+          while (my >= ns) {
+            my -= ns;
+            my_phase ^= 1;
+          }
+          // kKvBatch units at a time, every lane for itself: a stage is filled
+          // as soon as the batch's last one is free
+          for (int b0 = 0; b0 < found && ok; b0 += kKvBatch) {
+            const bool go = busy && place >= b0 && place < b0 + kKvBatch;
+            bool got = true;
+            if (go) got = mbar_wait_bounded(&empty[my], my_phase, s_abort, a.status);
+            ok = __all_sync(0xFFFFFFFFu, got);
+            if (!ok) break;
+            if (go) {
+              if (MULTI) {  // entries of the page's keys
+                const int k = lane - unit * pl.ppt;
+                for (int i = 0; i < a.P; ++i) {
+                  pages[my * L::kPages + k * pl.pitch + i] = pg;
+                  poss[my * L::kPages + k * pl.pitch + i] = valid ? pos + i : INT32_MAX;
+                }
+              } else {
+                pages[my] = pg;
+                poss[my] = pos;
+              }
+              if (leads) {
+                const bool f = (fmask & who) == who && (!MULTI || pl.ppt * a.P == kKvUnit);
+                meta[my * 4] = sidx;
+                meta[my * 4 + 1] = f ? kKvFull : 0;
+                meta[my * 4 + 2] = nk;
+              }
             }
-            const int leader = __ffs(who) - 1;
-            if (lane == leader) {
-              int f = (fmask & who) == who ? kKvFull : 0;
-              if (MULTI && pl.ppt * a.P != kKvUnit) f = 0;
-              meta[slot * 4] = sidx;
-              meta[slot * 4 + 1] = f;
-              meta[slot * 4 + 2] = MULTI ? 0 : nk;
-            }
-            __syncwarp();
-            if (lane == leader)
-              mbar_arrive_expect_tx(&full[slot],
-                                    (uint32_t)__popc(vmask & who) * 2u * L::NB * L::RB *
-                                        (uint32_t)pl.box);
-            __syncwarp();
-            if (in && valid) {
-              unsigned char* dst = ring + (size_t)slot * L::kStage + (MULTI ? k * pl.pitch : 0) * L::RB;
+            if (MULTI) __syncwarp();
+            if (go && leads)
+              mbar_arrive_expect_tx(&full[my], (uint32_t)__popc(vmask & who) * 2u * L::NB * L::RB *
+                                                   (uint32_t)pl.box);
+            if (MULTI) __syncwarp();
+            if (go && valid) {
+              unsigned char* dst = ring + (size_t)my * L::kStage +
+                                   (MULTI ? (lane - unit * pl.ppt) * pl.pitch : 0) * L::RB;
 #pragma unroll
               for (int cb = 0; cb < L::NB; ++cb) {
-                tma_load_2d(dst + cb * kKvUnit * L::RB, &map_k, cb * L::RB, row, &full[slot]);
-                tma_load_2d(dst + (L::NB + cb) * kKvUnit * L::RB, &map_v, cb * L::RB, row,
-                            &full[slot]);
+                tma_load_2d(dst + cb * kKvUnit * L::RB, &map_k, cb * L::RB, row, &full[my]);
+                tma_load_2d(dst + (L::NB + cb) * kKvUnit * L::RB, &map_v, cb * L::RB, row, &full[my]);
               }
             }
             __syncwarp();
-            advance();
-            ++emitted;
           }
-        }
-        if (ok && emitted == 0 && acquire()) {  // a segment without keys still has its stage
-          if (lane == 0) {
-            meta[slot * 4] = sidx;
-            meta[slot * 4 + 1] = 0;
-            meta[slot * 4 + 2] = 0;
+          if (ok && busy && valid) {
+            last1 = last0;
+            par1 = par0;
+            last0 = &full[my];
+            par0 = my_phase ^ 1;
           }
-          if (lane < L::kPages) {
-            pages[slot * L::kPages + lane] = KvPage{0.f, 0.f, 0.f, 0.f};
-            poss[slot * L::kPages + lane] = INT32_MAX;
+          if (ok && none) {
+            ok = __all_sync(0xFFFFFFFFu,
+                            mbar_wait_bounded(&empty[slot], phase, s_abort, a.status));
+            if (!ok) break;
+            if (lane < L::kPages) {
+              pages[slot * L::kPages + lane] = KvPage{0.f, 0.f, 0.f, 0.f};
+              poss[slot * L::kPages + lane] = INT32_MAX;
+            }
+            if (lane == 0) {
+              meta[slot * 4] = sidx;
+              meta[slot * 4 + 1] = 0;
+              meta[slot * 4 + 2] = 0;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[slot]);
+            __syncwarp();
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[slot]);
-          __syncwarp();
-          advance();
-        }
+          // Only now the next look-up may issue: the one bit of a barrier's
+          // phase tells neighbouring passes over the ring apart, so stages are
+          // filled strictly in order.
+          if (ok) tell(used + n);
+          ++look;
+          c += tpc;
+        } while (c < stop && ok);
         ++sidx;
         u += t1 - t0;
       }
       base = rt_end;
       ++rt;
     }
-    // a last stage for each group of warps, then the copies in flight
-    for (int i = 0; i < KG && ok; ++i) {
-      if (!acquire()) break;
-      if (lane == 0) {
-        meta[slot * 4] = INT32_MAX;
-        mbar_arrive(&full[slot]);
-      }
-      __syncwarp();
-      advance();
-    }
-    if (lane == 0) {
-      int s = slot, ph = phase;  // walk back over the stages in use
-      for (int64_t i = 0; i < issued && i < ns; ++i) {
-        if (--s < 0) {
-          s = ns - 1;
-          ph ^= 1;
+    // a last stage for each group of warps
+    if (ok && look % kKvProducers == (uint32_t)pw) {
+      uint32_t used = 0;
+      ok = __all_sync(0xFFFFFFFFu, stages_before(used));
+      for (int i = 0; i < KG && ok; ++i, ++used) {
+        const int slot = (int)(used % (uint32_t)ns), phase = (int)((used / (uint32_t)ns) & 1) ^ 1;
+        ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[slot], phase, s_abort, a.status));
+        if (ok && lane == 0) {
+          meta[slot * 4] = INT32_MAX;
+          mbar_arrive(&full[slot]);
         }
-        mbar_wait_drain(&full[s], ph ^ 1);
+        __syncwarp();
       }
+    }
+    // The consumers wait for every stage; where they gave up, this lane's
+    // copies in flight end first (a stage used again since counts as ended).
+    if (!ok) {
+      for (int i = 0; last1 && i < (1 << 20) && !mbar_test_wait(last1, par1); ++i) {}
+      for (int i = 0; last0 && i < (1 << 20) && !mbar_test_wait(last0, par0); ++i) {}
     }
     if (bits) atomicOr(a.status, bits);
     return;

@@ -359,6 +359,13 @@ def test_attention_long_rows_few(ctx):
     check_attn(ctx, attn_case(12, 6, 1, 4, 1, 64, 16, 600, "int8", [[9600], [1], [0], [31], [5000], [33]]))
 
 
+@pytest.mark.parametrize("D,K", [(16, 0), (128, 0), (128, 900)])
+def test_attention_many_units_per_sm(ctx, D, K):
+    # hundreds of 32-key units on every SM: the ring of stages goes round many times
+    N = 960
+    check_attn(ctx, attn_case(27, 10, 1, 1, 1, D, 64, N, "e4m3", [[N * 64 - 9 * b] for b in range(10)], K=K))
+
+
 def test_attention_many_short_rows(ctx):
     rng = np.random.default_rng(13)
     check_attn(ctx, attn_case(13, 700, 1, 2, 1, 16, 8, 3, "e4m3", rng.integers(0, 25, (700, 1))))
