@@ -20,20 +20,21 @@
 // Work: a row tile is TT tokens of one request (1 with page lists, which differ
 // by token) and up to 16*MT query rows (tokens x heads of one kv head), an item
 // is a row tile and a kv head, a unit is 32 keys of it.  The units of all items
-// are laid end to end and cut evenly over the CTAs (one per SM).  An item that
+// are laid end to end, with a charge for each item's start and end, and cut
+// evenly over the CTAs (one per SM).  An item that
 // is cut leaves partial results (O, m, l) in the workspace; the last of its
 // CTAs to arrive joins them in the order of the keys.
 //
-// A CTA has four producer warps and eight consumer warps.  A producer looks up
+// A CTA has four producer warps and twelve consumer warps.  A producer looks up
 // 32 units at a time (page list, block table, scales; one per lane), skips
 // those without keys, and has the TMA engine copy the keys and values of each
 // into a ring of stages.  The producers take the look-ups in turns, so that
 // four chains of dependent loads are under way; they fill the stages in order,
 // each passing the number used so far to the next.  Consumer warp w works on the 16 query rows w % MT of
-// every (8/MT)th stage with an accumulator of its own, so no two warps meet
+// every (12/MT)th stage with an accumulator of its own, so no two warps meet
 // before the item's end; there they join their maxima, sums and accumulators.
-// (Above 128 columns two warps share a stage: each takes the scores, and half
-// of the value columns, which is what its registers hold.)
+// (Above 128 columns there are eight, and two share a stage: each takes the
+// scores, and half of the value columns, which is what its registers hold.)
 // One unit is 32 keys x D codes of K and of V: 8 KB at D = 128.
 //
 // The matrix instruction is the warp-wide m16n8k16: with few query rows a key
@@ -48,17 +49,18 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "kv.cuh"
 #include "tc.cuh"
 
 namespace idx {
 
-constexpr int kKvConsumers = 8;
 constexpr int kKvProducers = 4;
-constexpr int kKvThreads = (kKvConsumers + kKvProducers) * 32;
 constexpr int kKvUnit = 32;        // keys per unit
 constexpr int kKvMaxStages = 32;
 constexpr int kKvBatch = 4;        // units the producer issues at once
+constexpr int kKvCharge = 8;       // units that an item's start and end count for in the split
 constexpr int kKvSegs = 64;        // descriptor ring: more than the stages and a group of warps
 constexpr int kKvSmem = 227 * 1024;
 constexpr float kKvMinScale = 7.8886090522101181e-31f;  // 2^-100
@@ -79,7 +81,7 @@ struct KvPlan {
 constexpr int kKvSlot = 64 * 256 + 128;  // floats of a workspace slot
 
 struct KvSeg {
-  int64_t unit0;    // the item's first unit
+  int64_t unit0;    // the item's first unit, as the split counts
   int nt;           // its units
   int b, t0, nrow;  // request, first token, query rows (tokens x heads)
   int h0;           // first query head
@@ -102,9 +104,17 @@ struct KvLayout {
   static constexpr int NB = DP / RB;                  // column blocks
   static constexpr int NH = DP == 256 ? 2 : 1;        // warps that share a unit's value columns
   static constexpr int OC = DP / NH;                  // value columns of a warp
-  static constexpr int KG = kKvConsumers / (MT * NH); // groups of warps taking turns
+  // Above 128 columns two warps share a unit, and eight warps divide evenly over
+  // pairs and row groups.
+  static constexpr int NC = DP == 256 ? 8 : 12;       // consumer warps
+  static constexpr int NT = (NC + kKvProducers) * 32; // threads
+  static constexpr int KG = NC / (MT * NH);           // groups of warps taking turns
+  // The launch's registers (128 or 168 a thread), moved from the producers to
+  // the consumers: 4 x 80 + 12 x 144 = 16 x 128, 4 x 80 + 8 x 208 <= 12 x 168.
+  static constexpr int kProducerRegs = 80;
+  static constexpr int kConsumerRegs = DP == 256 ? 208 : 144;
   static constexpr int kStage = 2 * kKvUnit * DP;     // K then V
-  static constexpr int CM = DP == 256 ? 64 : OC;      // columns of a warp joined at a time
+  static constexpr int CM = 32;                       // columns of a warp joined at a time
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int kPages = MULTI ? kKvUnit : 1;  // scale entries: per key or one
   static constexpr size_t bars = 0;                                    // full, empty
@@ -114,11 +124,11 @@ struct KvLayout {
   static constexpr size_t page = meta + kKvMaxStages * 16;
   static constexpr size_t pos = page + (size_t)kKvMaxStages * kPages * sizeof(KvPage);
   static constexpr size_t ml = (pos + (size_t)kKvMaxStages * kPages * 4 + 15) & ~(size_t)15;
-  static constexpr size_t rows = ml + kKvConsumers * 16 * 8;           // factor, limit per row
-  static constexpr size_t q = rows + 64 * 12;
+  static constexpr size_t rows = ml + NC * 16 * 8;           // factor, limit per row
+  static constexpr size_t q = rows + 64 * 20;
   static constexpr size_t join = q + (size_t)16 * MT * kQPitch;
   static constexpr size_t ring =
-      (join + (size_t)kKvConsumers * 16 * (CM + 4) * 4 + 1023) & ~(size_t)1023;
+      (join + (size_t)NC * 16 * (CM + 4) * 4 + 1023) & ~(size_t)1023;
   static constexpr int stages() {
     const int n = (int)((kKvSmem - 1024 - ring) / kStage);
     return n < kKvMaxStages ? n : kKvMaxStages;
@@ -130,7 +140,7 @@ struct KvLayout {
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                         uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -142,6 +152,10 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -228,12 +242,12 @@ __device__ __forceinline__ KvTile kv_tile(const KvAttnArgs& a, const KvPlan& pl,
 }
 
 template <int FMT, int DP, int MT, bool MULTI>
-__global__ void __launch_bounds__(kKvThreads, 1)
+__global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const KvAttnArgs a,
                    const KvPlan pl) {
   using L = KvLayout<DP, MT, MULTI>;
-  constexpr int KG = L::KG;
+  constexpr int KG = L::KG, NC = L::NC;
   constexpr int M = 16 * MT;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -246,7 +260,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   int64_t* s_where = reinterpret_cast<int64_t*>(misc + 8);  // row tile, units before, both ends
   long long* s_warp = reinterpret_cast<long long*>(misc + 24);  // warp sums
   volatile unsigned long long* s_tot =  // per look-up: its number, stages before it
-      reinterpret_cast<volatile unsigned long long*>(misc + 48);
+      reinterpret_cast<volatile unsigned long long*>(misc + 56);
   KvSeg* segs = reinterpret_cast<KvSeg*>(smem + L::seg);
   int* meta = reinterpret_cast<int*>(smem + L::meta);
   KvPage* pages = reinterpret_cast<KvPage*>(smem + L::page);
@@ -259,11 +273,20 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   int bits = 0;
 
   // ---- the split: units before each thread's row tiles, then this CTA's share
-  const int64_t per = (nrt + kKvThreads - 1) / kKvThreads;
+  const int64_t per = (nrt + L::NT - 1) / L::NT;
   const int64_t rt0 = tid * per < nrt ? tid * per : nrt;
   const int64_t rt1 = rt0 + per < nrt ? rt0 + per : nrt;
   long long mine = 0;
-  for (int64_t rt = rt0; rt < rt1; ++rt) mine += kv_tile(a, pl, rt, bits).nt;
+  if (tid == 0) {
+    prefetch_map(&map_k);
+    prefetch_map(&map_v);
+  }
+  int nt_first = 0;
+  for (int64_t rt = rt0; rt < rt1; ++rt) {
+    const int nt = kv_tile(a, pl, rt, bits).nt;
+    if (rt == rt0) nt_first = nt;
+    mine += nt + kKvCharge;
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -279,13 +302,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   if (tid == 0) *s_abort = 0;
   if (tid < kKvProducers) s_tot[tid] = tid ? ~0ull : 0ull;
   if (MULTI)  // rows between and behind a unit's pages hold no key
-    for (int i = tid; i < kKvMaxStages * L::kPages; i += kKvThreads) {
+    for (int i = tid; i < kKvMaxStages * L::kPages; i += L::NT) {
       pages[i] = KvPage{0.f, 0.f, 0.f, 0.f};
       poss[i] = INT32_MAX;
     }
   __syncthreads();
   long long before = 0, total = 0;
-  for (int w = 0; w < kKvThreads / 32; ++w) {
+  for (int w = 0; w < L::NT / 32; ++w) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
@@ -293,7 +316,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   const int64_t W = total * items;
   // at least a unit for each group of warps, so that a short batch is not cut
   // into more parts than joining them is worth
-  int64_t nc = W / KG;
+  int64_t nc = W / (KG + kKvCharge);
   nc = nc < 1 ? 1 : (nc < (int64_t)gridDim.x ? nc : (int64_t)gridDim.x);
   if ((int64_t)blockIdx.x >= nc) return;
   if (tid == 0) {
@@ -305,23 +328,28 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     long long base = before * items;
     if (u_begin < base + mine * items && u_end > base)
       for (int64_t rt = rt0; rt < rt1; ++rt) {
-        const int64_t n = (int64_t)kv_tile(a, pl, rt, bits).nt * items;
-        if (u_begin >= base && u_begin < base + n) {
+        const int64_t n = (rt == rt0 ? nt_first : kv_tile(a, pl, rt, bits).nt) + kKvCharge;
+        if (u_begin >= base && u_begin < base + n * items) {
           s_where[0] = rt;
           s_where[1] = base;
-          s_where[4] = rt * items + (u_begin - base) / (n / items);
+          s_where[4] = rt * items + (u_begin - base) / n;
         }
-        if (u_end - 1 >= base && u_end - 1 < base + n)
-          s_where[5] = rt * items + (u_end - 1 - base) / (n / items);
-        base += n;
+        if (u_end - 1 >= base && u_end - 1 < base + n * items) {
+          // a last item of which only charged units fall here is not this CTA's
+          const int64_t it = (u_end - 1 - base) / n;
+          s_where[5] = rt * items + it - (u_end - base - it * n <= kKvCharge ? 1 : 0);
+        }
+        base += n * items;
       }
   }
   __syncthreads();
   const int nseg = (int)(s_where[5] - s_where[4] + 1);
+  if (nseg <= 0) return;
 
-  if (warp >= kKvConsumers) {
+  if (warp >= NC) {
     // =================================================================== producers
-    const int pw = warp - kKvConsumers;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kProducerRegs));
+    const int pw = warp - NC;
     int64_t rt = s_where[0], base = s_where[1], u = u_begin;
     uint32_t look = 0;            // look-ups so far, of all producers
     int sidx = 0;
@@ -363,11 +391,17 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       mx = __reduce_max_sync(0xFFFFFFFFu, mx);
       mn = __reduce_min_sync(0xFFFFFFFFu, mn);
       const int nt = kv_units(a, pl, mx);
-      const int64_t rt_end = base + (int64_t)nt * items;
+      const int64_t n = nt + kKvCharge;
+      const int64_t rt_end = base + n * items;
       while (ok && u < u_end && u < rt_end) {
-        const int it = (int)((u - base) / nt);
-        const int t0 = (int)((u - base) - (int64_t)it * nt);
-        const int t1 = nt - t0 < u_end - u ? nt : t0 + (int)(u_end - u);
+        const int it = (int)((u - base) / n);
+        const int64_t x0 = (u - base) - it * n;
+        const int64_t x1 = n - x0 < u_end - u ? n : x0 + (u_end - u);
+        u += x1 - x0;
+        // the charged units come first: a cut among them is a cut before the item
+        const int t0 = x0 <= kKvCharge ? 0 : (int)(x0 - kKvCharge);
+        const int t1 = x1 <= kKvCharge ? 0 : (int)(x1 - kKvCharge);
+        if (t1 == t0) continue;
         const int g = it / pl.ng, hg = it - g * pl.ng;
         const int G = a.Q / a.H;
         const int heads = G - hg * pl.GG < pl.GG ? G - hg * pl.GG : pl.GG;
@@ -446,13 +480,13 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           const uint32_t lead = __ballot_sync(0xFFFFFFFFu, leads);
           const int found = __popc(lead);
           const bool none = found == 0 && c == t0;
-          const int n = none ? 1 : found;
+          const int fill = none ? 1 : found;
           uint32_t used = 0;
           ok = __all_sync(0xFFFFFFFFu, stages_before(used));
           if (!ok) break;
           if (c == t0 && lane == 0) {
             KvSeg& s = segs[sidx % kKvSegs];
-            s.unit0 = base + (int64_t)it * nt;
+            s.unit0 = base + it * n + kKvCharge;
             s.nt = nt;
             s.b = b;
             s.t0 = tk;
@@ -537,12 +571,11 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           // Only now the next look-up may issue: the one bit of a barrier's
           // phase tells neighbouring passes over the ring apart, so stages are
           // filled strictly in order.
-          if (ok) tell(used + n);
+          if (ok) tell(used + fill);
           ++look;
           c += tpc;
         } while (c < stop && ok);
         ++sidx;
-        u += t1 - t0;
       }
       base = rt_end;
       ++rt;
@@ -572,6 +605,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   }
 
   // ===================================================================== consumers
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kConsumerRegs));
   const int mt = warp % MT, half = (warp / MT) % L::NH, kg = warp / (MT * L::NH);
   const int g8 = lane >> 2, c4 = lane & 3;  // row and column quad of a fragment
   constexpr bool PERM = DP >= 128;
@@ -579,69 +613,81 @@ __global__ void __launch_bounds__(kKvThreads, 1)
   auto key_of = [&](int e) { return PERM ? c4 + 4 * e : 2 * c4 + e; };
   const int krow = PERM ? (g8 >> 1) + 4 * (g8 & 1) : g8;
   float* s_m = reinterpret_cast<float*>(smem + L::ml);
-  float* s_l = s_m + kKvConsumers * 16;
+  float* s_l = s_m + NC * 16;
   float* s_qf = reinterpret_cast<float*>(smem + L::rows);
   int* s_lims = reinterpret_cast<int*>(s_qf + 64);
+  float* s_rowm = reinterpret_cast<float*>(s_lims + 128);  // the joined rows' m and l
+  float* s_rowl = s_rowm + 64;
   unsigned char* s_q = smem + L::q;
   float* s_join = reinterpret_cast<float*>(smem + L::join);
   int slot = kg, phase = 0;
   bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot], phase, s_abort, a.status));
   int cur = ok ? meta[slot * 4] : INT32_MAX;
 
+  // queries of a segment: a warp per row, loaded while the one before it is
+  // joined, then normalised to a power of two and written as fp16
+  constexpr int QR = (M + NC - 1) / NC;
+  const int G = a.Q / a.H;
+  uint4 qv[QR];
+  int qlim[QR];
+  auto load_q = [&](const KvSeg& sg) {
+    const int nh = G - sg.h0 % G < pl.GG ? G - sg.h0 % G : pl.GG;  // heads of the item
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+      const int m = warp + i * NC;
+      qv[i] = make_uint4(0u, 0u, 0u, 0u);
+      qlim[i] = 0;
+      if (m < sg.nrow) {
+        const int tt = m / nh;
+        const int64_t r = (int64_t)sg.b * a.T + sg.t0 + tt;
+        qlim[i] = kv_count(a, r, bits);
+        if (lane * 8 < a.D)
+          qv[i] = __ldg(reinterpret_cast<const uint4*>(
+              a.q + r * a.ldq + (int64_t)(sg.h0 + m - tt * nh) * a.D + lane * 8));
+      }
+    }
+  };
+  auto store_q = [&](int* s_lim) {
+#pragma unroll
+    for (int i = 0; i < QR; ++i) {
+      const int m = warp + i * NC;
+      if (m >= M) break;
+      const uint32_t w[4] = {qv[i].x, qv[i].y, qv[i].z, qv[i].w};
+      uint32_t top = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
+        top = lo < 0x7F80u && lo > top ? lo : top;
+        top = hi < 0x7F80u && hi > top ? hi : top;
+      }
+      int e = (int)(__reduce_max_sync(0xFFFFFFFFu, top) >> 7);  // exponent field of the largest
+      e = e < 1 ? 1 : (e > 252 ? 252 : e);
+      const float f = __int_as_float((254 - e) << 23);  // 2^(127 - e)
+      uint32_t o[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        o[k] = pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
+      if (lane * 8 < DP)
+        *reinterpret_cast<uint4*>(s_q + m * L::kQPitch + lane * 16) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      if (lane == 0) {
+        s_qf[m] = a.scale * 1.44269504088896340736f * __int_as_float(e << 23);
+        s_lim[m] = qlim[i];
+      }
+    }
+  };
+  if (ok) load_q(segs[0]);
+
   for (int s = 0; s < nseg; ++s) {
     // On an expired wait (cur is then "past every segment") the descriptors may
     // be missing: the warps still meet at every barrier, and write nothing.
     const KvSeg& sg = segs[s % kKvSegs];
     int* s_lim = s_lims + (s & 1) * 64;  // still read when the next item's is written
-    // ---- queries: a warp per row, normalised to a power of two, as fp16
-    {
-      const int G = a.Q / a.H;
-      const int hh = sg.h0 % G;
-      const int nh = G - hh < pl.GG ? G - hh : pl.GG;  // heads of this item
-#pragma unroll
-      for (int i = 0; i < M / kKvConsumers; ++i) {
-        const int m = warp + i * kKvConsumers;
-        uint4 v = make_uint4(0u, 0u, 0u, 0u);
-        int lim = 0;
-        if (ok && m < sg.nrow) {
-          const int tt = m / nh;
-          const int64_t r = (int64_t)sg.b * a.T + sg.t0 + tt;
-          int dummy = 0;
-          lim = kv_count(a, r, dummy);
-          if (lane * 8 < a.D)
-            v = __ldg(reinterpret_cast<const uint4*>(a.q + r * a.ldq +
-                                                     (int64_t)(sg.h0 + m - tt * nh) * a.D + lane * 8));
-        }
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
-          top = lo < 0x7F80u && lo > top ? lo : top;
-          top = hi < 0x7F80u && hi > top ? hi : top;
-        }
-        int e = (int)(__reduce_max_sync(0xFFFFFFFFu, top) >> 7);  // exponent field of the largest
-        e = e < 1 ? 1 : (e > 252 ? 252 : e);
-        const float f = __int_as_float((254 - e) << 23);  // 2^(127 - e)
-        uint32_t o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = pack_f16(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xFFFF0000u) * f);
-        if (lane * 8 < DP)
-          *reinterpret_cast<uint4*>(s_q + m * L::kQPitch + lane * 16) = make_uint4(o[0], o[1], o[2], o[3]);
-        if (lane == 0) {
-          s_qf[m] = a.scale * 1.44269504088896340736f * __int_as_float(e << 23);
-          s_lim[m] = lim;
-        }
-      }
-    }
-    group_sync(kKvConsumers * 32);
+    store_q(s_lim);
+    group_sync(NC * 32);
     const int row0 = mt * 16 + g8;
     const float qf0 = s_qf[row0], qf1 = s_qf[row0 + 8];
     const int lim0 = s_lim[row0], lim1 = s_lim[row0 + 8];
-    constexpr bool QREG = DP <= 128;
-    constexpr int NQ = QREG ? DP / 16 : 1;
-    uint32_t qa[NQ][4];
     // operand of k step i (16 dims) of 64-dim half h: dims 64 h + 16 c4 + 4 i ..
     auto load_q2 = [&](int hi2, uint32_t (&x)[4], uint32_t (&y)[4]) {
       // two steps at once: hi2 = (64-dim half) * 2 + pair
@@ -652,10 +698,6 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       x[0] = u0.x; x[2] = u0.y; y[0] = u0.z; y[2] = u0.w;
       x[1] = u1.x; x[3] = u1.y; y[1] = u1.z; y[3] = u1.w;
     };
-    if (QREG) {
-#pragma unroll
-      for (int i = 0; i < NQ / 2; ++i) load_q2(i, qa[2 * i], qa[2 * i + 1]);
-    }
     float oacc[L::OC / 16][2][4];
 #pragma unroll
     for (int j = 0; j < L::OC / 16; ++j)
@@ -665,38 +707,41 @@ __global__ void __launch_bounds__(kKvThreads, 1)
         for (int k = 0; k < 4; ++k) oacc[j][e][k] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-    while (cur == s) {
+    // One stage; FULL: no row that sees any key misses one of these.
+    auto unit = [&](auto full_tag) {
+      constexpr bool is_full = decltype(full_tag)::value;
       const unsigned char* kb_ = ring + (size_t)slot * L::kStage;
       const uint32_t vb_ = smem_u32(kb_) + kKvUnit * DP;
-      const bool is_full = (meta[slot * 4 + 1] & kKvFull) != 0;
-      const int nk = meta[slot * 4 + 2];
+      const int nk = is_full ? kKvUnit : meta[slot * 4 + 2];
       // ---- scores
       float sc[4][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int x = 0; x < 4; ++x) sc[k][x] = 0.f;
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < DP / 64; ++h) {
-        uint32_t q4[4][4];
-        if (!QREG) {
-          load_q2(2 * h, q4[0], q4[1]);
-          load_q2(2 * h + 1, q4[2], q4[3]);
-        }
+        uint4 w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = k * 8 + krow;
           const int chunk = DP == 64 ? (c4 ^ ((row >> 1) & 3)) : (((h & 1) * 4 + c4) ^ (row & 7));
-          const uint4 w = *reinterpret_cast<const uint4*>(
+          w[k] = *reinterpret_cast<const uint4*>(
               kb_ + (DP == 256 ? (h >> 1) * kKvUnit * 128 : 0) + row * L::RB + chunk * 16);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        }
+        // four keys' products side by side: each waits for its own last one only
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t b0, b1;
-            codes4<FMT, false>(ww[i], b0, b1);
-            if (QREG) mma_f16(sc[k], qa[QREG ? h * 4 + i : 0], b0, b1);
-            else mma_f16(sc[k], q4[i], b0, b1);
-          }
+        for (int i2 = 0; i2 < 2; ++i2) {
+          uint32_t q4[2][4];
+          load_q2(2 * h + i2, q4[0], q4[1]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t b0, b1;
+              codes4<FMT, false>(i2 ? (i ? w[k].w : w[k].z) : (i ? w[k].y : w[k].x), b0, b1);
+              mma_f16(sc[k], q4[i], b0, b1);
+            }
         }
       }
       // ---- scales, masks, running maximum
@@ -731,7 +776,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           sc[k][3] = fmaf(sc[k][3], f1, pg.lv);
         }
       }
-      if (!is_full) {
+      if constexpr (!is_full) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int j = (i >> 1) * 8 + key_of(i & 1);
@@ -790,7 +835,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       }
       // ---- O += P V
       uint32_t keep[4];  // bytes of this lane's two keys that some row sees
-      if (!is_full) {
+      if constexpr (!is_full) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           keep[k] = 0;
@@ -814,7 +859,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           const int chunk = DP == 64 ? (ch ^ ((row >> 1) & 3)) : ((ch & 7) ^ (row & 7));
           uint32_t r[4];
           ldsm4_t(r, vb_ + half * (kKvUnit * 128) + row * L::RB + chunk * 16);
-          if (!is_full) {
+          if constexpr (!is_full) {
             r[0] &= keep[2 * kk];
             r[1] &= keep[2 * kk + 1];
             r[2] &= keep[2 * kk];
@@ -868,6 +913,10 @@ __global__ void __launch_bounds__(kKvThreads, 1)
           }
         }
       }
+    };
+    while (cur == s) {
+      if (meta[slot * 4 + 1] & kKvFull) unit(std::true_type());
+      else unit(std::false_type());
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[slot]);
       slot += KG;
@@ -891,7 +940,7 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       s_l[warp * 16 + g8 + 8] = l1;
     }
     if (tid == 0) s_flag[0] = *s_abort;
-    group_sync(kKvConsumers * 32);
+    group_sync(NC * 32);
     const bool aborted = s_flag[0] != 0;
     float mm0 = -INFINITY, mm1 = -INFINITY;
 #pragma unroll
@@ -901,74 +950,91 @@ __global__ void __launch_bounds__(kKvThreads, 1)
     }
     const float f0 = m0 == -INFINITY ? (l0 == l0 ? 0.f : l0) : ex2(m0 - mm0);
     const float f1 = m1 == -INFINITY ? (l1 == l1 ? 0.f : l1) : ex2(m1 - mm1);
-    const int part = sg.first && sg.last ? 0 : 1;  // the item is in several CTAs
+    const bool part = !(sg.first && sg.last);  // the item is in several CTAs
     float* wslot = pl.ws + (int64_t)(2 * blockIdx.x + (sg.first ? 1 : 0)) * kKvSlot;
-    const int G = a.Q / a.H;
     const int nh = G - sg.h0 % G < pl.GG ? G - sg.h0 % G : pl.GG;
-    constexpr int CM = L::CM, JP = CM + 4;
-    constexpr int CPR = CM / 8;  // 8-column pieces of a row
+    // four columns of a row, joined, to their places
+    auto finish = [&](int row, int oc, float m, float l, const float4& o) {
+      const int tt = row / nh;
+      const int64_t rq = ((int64_t)sg.b * a.T + sg.t0 + tt) * a.Q + sg.h0 + row - tt * nh;
+      const bool zero = l == 0.f;
+      auto two = [&](float x, float y) {
+        return zero ? 0u
+                    : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(x, l))) |
+                          ((uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(y, l))) << 16);
+      };
+      *reinterpret_cast<uint2*>(a.out + rq * a.D + oc) = make_uint2(two(o.x, o.y), two(o.z, o.w));
+      if (oc == 0 && a.lse)
+        a.lse[rq] = zero ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+    };
+    auto own_factor = [&](float mk, float lk, float m) {  // 0 for no keys, NaN stays
+      return mk == -INFINITY ? (lk == lk ? 0.f : lk) : ex2(mk - m);
+    };
+    if (tid < sg.nrow && !aborted) {
+      const int rm = tid & 15, rg = tid >> 4;
+      float m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int cb = 0; cb < L::OC / CM; ++cb) {
-      if (cb) group_sync(kKvConsumers * 32);
+      for (int k = 0; k < KG; ++k) m = fmaxf(m, s_m[(k * L::NH * MT + rg) * 16 + rm]);
 #pragma unroll
-      for (int j = 0; j < CM / 16; ++j) {
-        float* d = s_join + (warp * 16 + g8) * JP + j * 16 + c4 * 4;
-        auto& o = oacc[cb * (CM / 16) + j];
-        *reinterpret_cast<float4*>(d) =
-            make_float4(o[0][0] * f0, o[1][0] * f0, o[0][1] * f0, o[1][1] * f0);
-        *reinterpret_cast<float4*>(d + 8 * JP) =
-            make_float4(o[0][2] * f1, o[1][2] * f1, o[0][3] * f1, o[1][3] * f1);
+      for (int k = 0; k < KG; ++k) {
+        const float mk = s_m[(k * L::NH * MT + rg) * 16 + rm], lk = s_l[(k * L::NH * MT + rg) * 16 + rm];
+        l = fmaf(mk == -INFINITY ? (lk == lk ? 0.f : 1.f) : lk, own_factor(mk, lk, m), l);
       }
-      group_sync(kKvConsumers * 32);
-      for (int i = tid; i < M * L::NH * CPR; i += kKvConsumers * 32) {
-        const int row = i / (L::NH * CPR), hf = (i / CPR) % L::NH, col = (i % CPR) * 8;
-        const int oc = hf * L::OC + cb * CM + col;  // the output column
-        if (aborted || row >= sg.nrow || oc >= a.D) continue;
-        const int rm = row & 15, rt16 = row >> 4;
-        float m = -INFINITY;
+      const bool none = s_lim[tid] == 0;  // padding: whatever its query gave
+      s_rowm[tid] = none ? -INFINITY : m;
+      s_rowl[tid] = none ? 0.f : l;
+    }
+    // The accumulators go through shared memory, as many columns at a time as
+    // its room holds of the rows in use.
+    const int rr = sg.nrow < 16 ? sg.nrow : 16;
+    int per = rr <= 4 ? 4 : (rr <= 8 ? 2 : 1);
+    per = per < L::OC / 32 ? per : L::OC / 32;
+    const int jp = per * 32 + 4;
 #pragma unroll
-        for (int k = 0; k < KG; ++k) m = fmaxf(m, s_m[(k * L::NH * MT + rt16) * 16 + rm]);
-        float l = 0.f, o[8];
+    for (int cb = 0; cb < L::OC / 32; ++cb) {
+      const int sub = cb & (per - 1);
 #pragma unroll
-        for (int x = 0; x < 8; ++x) o[x] = 0.f;
+      for (int j = 0; j < 2; ++j) {
+        const auto& o = oacc[cb * 2 + j];
+        float* d = s_join + (warp * rr + g8) * jp + sub * 32 + j * 16 + c4 * 4;
+        if (g8 < rr)
+          *reinterpret_cast<float4*>(d) =
+              make_float4(o[0][0] * f0, o[1][0] * f0, o[0][1] * f0, o[1][1] * f0);
+        if (g8 + 8 < rr)
+          *reinterpret_cast<float4*>(d + 8 * jp) =
+              make_float4(o[0][2] * f1, o[1][2] * f1, o[0][3] * f1, o[1][3] * f1);
+      }
+      if (sub != per - 1) continue;
+      group_sync(NC * 32);
+      const int pieces = per * 8;  // of four columns
+      for (int i = tid; i < sg.nrow * L::NH * pieces && !aborted; i += NC * 32) {
+        const int row = i / (L::NH * pieces), rem = i - row * (L::NH * pieces);
+        const int hf = rem / pieces, pc = rem - hf * pieces;
+        const int oc = hf * L::OC + (cb - sub) * 32 + pc * 4;  // the output column
+        if (oc >= a.D) continue;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
-          const int w = (k * L::NH + hf) * MT + rt16;
-          const float mw = s_m[w * 16 + rm], lw = s_l[w * 16 + rm];
-          l += mw == -INFINITY ? (lw == lw ? 0.f : lw) : lw * ex2(mw - m);
-          const float4 u0 = *reinterpret_cast<const float4*>(s_join + (w * 16 + rm) * JP + col);
-          const float4 u1 = *reinterpret_cast<const float4*>(s_join + (w * 16 + rm) * JP + col + 4);
-          o[0] += u0.x; o[1] += u0.y; o[2] += u0.z; o[3] += u0.w;
-          o[4] += u1.x; o[5] += u1.y; o[6] += u1.z; o[7] += u1.w;
+          const int w = (k * L::NH + hf) * MT + (row >> 4);
+          const float4 u = *reinterpret_cast<const float4*>(s_join + (w * rr + (row & 15)) * jp + pc * 4);
+          o.x += u.x;
+          o.y += u.y;
+          o.z += u.z;
+          o.w += u.w;
         }
-        const bool none = s_lim[row] == 0;
         if (part) {
-          float* d = wslot + row * 256 + oc;
-          *reinterpret_cast<float4*>(d) = make_float4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<float4*>(d + 4) = make_float4(o[4], o[5], o[6], o[7]);
+          *reinterpret_cast<float4*>(wslot + row * 256 + oc) = o;
           if (oc == 0) {
-            wslot[64 * 256 + row] = m;
-            wslot[64 * 256 + 64 + row] = none ? 0.f : l;
+            wslot[64 * 256 + row] = s_rowm[row];
+            wslot[64 * 256 + 64 + row] = s_rowl[row];
           }
         } else {
-          const int tt = row / nh;
-          const int64_t rq = ((int64_t)sg.b * a.T + sg.t0 + tt) * a.Q + sg.h0 + row - tt * nh;
-          const bool zero = none || l == 0.f;
-          uint32_t p[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            p[x] = zero ? 0u
-                        : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(o[2 * x], l))) |
-                              ((uint32_t)__bfloat16_as_ushort(
-                                   __float2bfloat16_rn(__fdiv_rn(o[2 * x + 1], l)))
-                               << 16);
-          *reinterpret_cast<uint4*>(a.out + rq * a.D + oc) =
-              make_uint4(p[0], p[1], p[2], p[3]);
-          if (oc == 0 && a.lse)
-            a.lse[rq] = zero ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+          finish(row, oc, s_rowm[row], s_rowl[row], o);
         }
       }
+      if (cb != L::OC / 32 - 1) group_sync(NC * 32);
     }
+    if (ok && s + 1 < nseg) load_q(segs[(s + 1) % kKvSegs]);
     if (part && !aborted) {
       // the item's CTAs: c0 holds its first unit, c1 its last
       const int64_t W = s_where[2], nc = s_where[3];
@@ -976,54 +1042,74 @@ __global__ void __launch_bounds__(kKvThreads, 1)
       const int64_t c1 = ((sg.unit0 + sg.nt) * nc + W - 1) / W - 1;
       const int np = (int)(c1 - c0) + 1;
       __threadfence();
-      group_sync(kKvConsumers * 32);
+      group_sync(NC * 32);
       if (tid == 0) {
         const int before_ = atomicAdd(pl.arrive + c0, 1);
         s_flag[1] = before_ == np - 1;
         if (before_ == np - 1) pl.arrive[c0] = 0;
       }
-      group_sync(kKvConsumers * 32);
+      group_sync(NC * 32);
       if (s_flag[1]) {
         __threadfence();
-        // part 0 is in the second slot of its CTA, the others in the first of theirs
-        auto at = [&](int i) {
-          return pl.ws + (int64_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * kKvSlot;
-        };
-        const int cpr = a.D / 8;
-        for (int i = tid; i < sg.nrow * cpr; i += kKvConsumers * 32) {
-          const int row = i / cpr, col = (i - row * cpr) * 8;
-          float m = -INFINITY;
-          for (int k = 0; k < np; ++k) m = fmaxf(m, __ldcg(at(k) + 64 * 256 + row));
-          float l = 0.f, o[8];
+        // Part 0 is in the second slot of its CTA, the others in the first of
+        // theirs.  Threads that the pieces leave over share the parts of a piece.
+        const float* ws0 = pl.ws + 2 * c0 * kKvSlot;
+        const int cpr = a.D / 4, np4 = sg.nrow * cpr;
+        int share = NC * 32 / np4;
+        share = share < 1 ? 1 : (share < np ? share : np);
+        for (int i0 = 0; i0 < np4; i0 += NC * 32) {
+          const int piece = share > 1 ? tid % np4 : i0 + tid, sh = share > 1 ? tid / np4 : 0;
+          const bool on = piece < np4 && sh < share;
+          const int row = piece / cpr, oc = (piece - row * cpr) * 4;
+          float m = -INFINITY, l = 0.f;
+          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+          auto add = [&](float mk, float lk, const float4& u) {
+            const float mn = fmaxf(m, mk);
+            const float fa = own_factor(m, l, mn), fb = own_factor(mk, lk, mn);
+            m = mn;
+            l = fmaf(l, fa, lk * fb);
+            o.x = fmaf(o.x, fa, u.x * fb);
+            o.y = fmaf(o.y, fa, u.y * fb);
+            o.z = fmaf(o.z, fa, u.z * fb);
+            o.w = fmaf(o.w, fa, u.w * fb);
+          };
+          constexpr int UP = 4;  // parts in flight
+          for (int k0 = sh; on && k0 < np; k0 += UP * share) {
+            float mk[UP], lk[UP];
+            float4 u[UP];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) o[x] = 0.f;
-          for (int k = 0; k < np; ++k) {
-            const float* p = at(k);
-            const float mk = __ldcg(p + 64 * 256 + row), lk = __ldcg(p + 64 * 256 + 64 + row);
-            const float f = mk == -INFINITY ? (lk == lk ? 0.f : lk) : ex2(mk - m);
-            const float4 u0 = __ldcg(reinterpret_cast<const float4*>(p + row * 256 + col));
-            const float4 u1 = __ldcg(reinterpret_cast<const float4*>(p + row * 256 + col + 4));
-            l = fmaf(lk, f, l);
-            o[0] = fmaf(u0.x, f, o[0]); o[1] = fmaf(u0.y, f, o[1]);
-            o[2] = fmaf(u0.z, f, o[2]); o[3] = fmaf(u0.w, f, o[3]);
-            o[4] = fmaf(u1.x, f, o[4]); o[5] = fmaf(u1.y, f, o[5]);
-            o[6] = fmaf(u1.z, f, o[6]); o[7] = fmaf(u1.w, f, o[7]);
+            for (int x = 0; x < UP; ++x) {
+              const int k = k0 + x * share;
+              if (k >= np) break;
+              const float* p = ws0 + (int64_t)(2 * k + (k == 0 ? 1 : 0)) * kKvSlot;
+              mk[x] = __ldcg(p + 64 * 256 + row);
+              lk[x] = __ldcg(p + 64 * 256 + 64 + row);
+              u[x] = __ldcg(reinterpret_cast<const float4*>(p + row * 256 + oc));
+            }
+#pragma unroll
+            for (int x = 0; x < UP; ++x)
+              if (k0 + x * share < np) add(mk[x], lk[x], u[x]);
           }
-          const int tt = row / nh;
-          const int64_t rq = ((int64_t)sg.b * a.T + sg.t0 + tt) * a.Q + sg.h0 + row - tt * nh;
-          const bool zero = l == 0.f;
-          uint32_t p[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            p[x] = zero ? 0u
-                        : (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(__fdiv_rn(o[2 * x], l))) |
-                              ((uint32_t)__bfloat16_as_ushort(
-                                   __float2bfloat16_rn(__fdiv_rn(o[2 * x + 1], l)))
-                               << 16);
-          *reinterpret_cast<uint4*>(a.out + rq * a.D + col) = make_uint4(p[0], p[1], p[2], p[3]);
-          if (col == 0 && a.lse)
-            a.lse[rq] = zero ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+          if (share > 1) {  // np4 * share <= the threads: one round
+            float* d = s_join + tid * 6;
+            group_sync(NC * 32);
+            if (on && sh > 0) {
+              d[0] = m;
+              d[1] = l;
+              d[2] = o.x;
+              d[3] = o.y;
+              d[4] = o.z;
+              d[5] = o.w;
+            }
+            group_sync(NC * 32);
+            for (int x = 1; on && sh == 0 && x < share; ++x) {
+              const float* p = s_join + (x * np4 + piece) * 6;
+              add(p[0], p[1], make_float4(p[2], p[3], p[4], p[5]));
+            }
+          }
+          if (on && sh == 0) finish(row, oc, m, l, o);
         }
+        group_sync(NC * 32);  // s_join is free again
       }
     }
   }
@@ -1043,7 +1129,7 @@ static cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, cons
   auto kern = kv_attn_kernel<FMT, DP, MT, MULTI>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, kKvThreads, smem, stream>>>(mk, mv, a, pl);
+  kern<<<grid, L::NT, smem, stream>>>(mk, mv, a, pl);
   return cudaGetLastError();
 }
 
