@@ -15,14 +15,13 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int num_sms, cudaStream_t stream
   const int G = a.Q / a.H;
   const int dp = a.D <= 64 ? 64 : (a.D <= 128 ? 128 : 256);
   KvPlan pl{};
-  // As few 16-row groups as hold the tile's query rows: the eight warps of a
-  // CTA share each unit's keys between that many of them, and every one decodes
-  // the codes for itself.  Tokens share a tile only where they share the keys.
+  // As few 8-row blocks as hold the tile's query rows.  Tokens share a tile only
+  // where they share the keys.
   pl.GG = G < 64 ? G : 64;
   pl.ng = (G + pl.GG - 1) / pl.GG;
   const int64_t rows = a.page_idx ? G : (int64_t)G * a.T;
-  const int mt = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
-  const int fit = 16 * mt / pl.GG;
+  const int nt = rows <= 8 ? 1 : 2, rg = rows <= 16 ? 1 : (rows <= 32 ? 2 : 4);
+  const int fit = 8 * nt * rg / pl.GG;
   pl.TT = a.page_idx || fit < 1 ? 1 : (fit < a.T ? fit : a.T);
   pl.ntb = (a.T + pl.TT - 1) / pl.TT;
   // A copy must start on 128 bytes of shared memory: 64-byte rows go in pairs.
@@ -46,9 +45,9 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int num_sms, cudaStream_t stream
                CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
-  if (dp == 64) return launch_kv_attn_dp<64>(mk, mv, a, pl, mt, num_sms, stream);
-  if (dp == 128) return launch_kv_attn_dp<128>(mk, mv, a, pl, mt, num_sms, stream);
-  return launch_kv_attn_dp<256>(mk, mv, a, pl, mt, num_sms, stream);
+  if (dp == 64) return launch_kv_attn_dp<64>(mk, mv, a, pl, nt, rg, num_sms, stream);
+  if (dp == 128) return launch_kv_attn_dp<128>(mk, mv, a, pl, nt, rg, num_sms, stream);
+  return launch_kv_attn_dp<256>(mk, mv, a, pl, nt, rg, num_sms, stream);
 }
 
 }  // namespace idx

@@ -25,26 +25,29 @@
 // is cut leaves partial results (O, m, l) in the workspace; the last of its
 // CTAs to arrive joins them in the order of the keys.
 //
-// A CTA has four producer warps and twelve consumer warps.  A producer looks up
-// 32 units at a time (page list, block table, scales; one per lane), skips
-// those without keys, and has the TMA engine copy the keys and values of each
-// into a ring of stages.  The producers take the look-ups in turns, so that
+// A CTA has four producer warps and twelve (or eight) consumer warps.  A producer
+// looks up 32 units at a time (page list, block table, scales; one per lane),
+// skips those without keys, and has the TMA engine copy the keys and values of
+// each into a ring of stages.  The producers take the look-ups in turns, so that
 // four chains of dependent loads are under way; they fill the stages in order,
-// each passing the number used so far to the next.  Consumer warp w works on the 16 query rows w % MT of
-// every (12/MT)th stage with an accumulator of its own, so no two warps meet
-// before the item's end; there they join their maxima, sums and accumulators.
-// (Above 128 columns there are eight, and two share a stage: each takes the
-// scores, and half of the value columns, which is what its registers hold.)
+// each passing the number used so far to the next.  A consumer warp takes every
+// 12th stage for up to 16 query rows (up to four warps share a stage when there are
+// more rows) with an accumulator of its own, so no two
+// warps meet before the item's end; there they join their maxima, sums and
+// accumulators.
 // One unit is 32 keys x D codes of K and of V: 8 KB at D = 128.
 //
-// The matrix instruction is the warp-wide m16n8k16: with few query rows a key
-// is used for 2 G flops a byte, far below what the tcgen05 tiles of 128 rows
-// are for, and the codes have to pass through registers to become fp16 anyway:
-// they go from there into the instruction without a second trip through shared
-// memory.  The order of the head dim within a product is free, so a lane takes
-// 16 consecutive codes of a key as four steps' operands; the keys of the
-// product with V come transposed out of ldmatrix as pairs of codes, which one
-// byte permute turns into two operands (even and odd dims).
+// The matrix instruction is the warp-wide m16n8k16, with the keys (of the
+// scores) and the value columns (of the outputs) as its 16 rows and the query
+// rows as its 8 columns: the 4 or 8 heads of a kv head fill them, and a code is
+// decoded once for all rows of a warp.  With so few query rows a key is used for
+// 4 flops a row and code, far below what the tcgen05 tiles of 128 rows are for,
+// and the codes have to pass through registers to become fp16 anyway: they go
+// from there into the instruction without a second trip through shared memory.
+// The order of the head dim within a product is free, so a lane takes 16
+// consecutive codes of a key as four steps' operands; the keys of the product
+// with V come transposed out of ldmatrix as pairs of codes, which one byte
+// permute turns into two operands (even and odd dims).
 #pragma once
 
 #include <cuda.h>
@@ -98,23 +101,23 @@ struct KvPage {
 };
 constexpr int kKvFull = 1;  // every row that sees any key sees all 32
 
-template <int DP, int MT, bool MULTI>
+// NT: 8-row blocks of query rows that a warp holds; RG: groups of warps over the
+// query rows (8 * NT * RG rows in all).
+template <int DP, int NT, int RG, bool MULTI>
 struct KvLayout {
   static constexpr int RB = DP < 128 ? DP : 128;      // bytes of a row in a block
   static constexpr int NB = DP / RB;                  // column blocks
-  static constexpr int NH = DP == 256 ? 2 : 1;        // warps that share a unit's value columns
-  static constexpr int OC = DP / NH;                  // value columns of a warp
-  // Above 128 columns two warps share a unit, and eight warps divide evenly over
-  // pairs and row groups.
   static constexpr int NC = DP == 256 ? 8 : 12;       // consumer warps
-  static constexpr int NT = (NC + kKvProducers) * 32; // threads
-  static constexpr int KG = NC / (MT * NH);           // groups of warps taking turns
+  static constexpr int kThreads = (NC + kKvProducers) * 32;
+  static constexpr int KG = NC / RG;                  // groups of warps taking turns
   // The launch's registers (128 or 168 a thread), moved from the producers to
   // the consumers: 4 x 80 + 12 x 144 = 16 x 128, 4 x 80 + 8 x 208 <= 12 x 168.
   static constexpr int kProducerRegs = 80;
-  static constexpr int kConsumerRegs = DP == 256 ? 208 : 144;
+  static constexpr int kConsumerRegs = NC == 8 ? 208 : 144;
+  static constexpr int WR = 8 * NT;                   // rows of a warp
+  static constexpr int M = WR * RG;                   // rows of a tile
   static constexpr int kStage = 2 * kKvUnit * DP;     // K then V
-  static constexpr int CM = 32;                       // columns of a warp joined at a time
+  static constexpr int kJoin = NC * (WR < 16 ? 16 : WR) * 36;  // floats to join accumulators in
   static constexpr int kQPitch = DP * 2 + 16;
   static constexpr int kPages = MULTI ? kKvUnit : 1;  // scale entries: per key or one
   static constexpr size_t bars = 0;                                    // full, empty
@@ -124,18 +127,18 @@ struct KvLayout {
   static constexpr size_t page = meta + kKvMaxStages * 16;
   static constexpr size_t pos = page + (size_t)kKvMaxStages * kPages * sizeof(KvPage);
   static constexpr size_t ml = (pos + (size_t)kKvMaxStages * kPages * 4 + 15) & ~(size_t)15;
-  static constexpr size_t rows = ml + NC * 16 * 8;           // factor, limit per row
+  static constexpr size_t rows = ml + NC * WR * 8;                     // factor, limits, m, l per row
   static constexpr size_t q = rows + 64 * 20;
-  static constexpr size_t join = q + (size_t)16 * MT * kQPitch;
-  static constexpr size_t ring =
-      (join + (size_t)NC * 16 * (CM + 4) * 4 + 1023) & ~(size_t)1023;
+  static constexpr size_t join = q + (size_t)M * kQPitch;
+  static constexpr size_t ring = (join + (size_t)kJoin * 4 + 1023) & ~(size_t)1023;
   static constexpr int stages() {
     const int n = (int)((kKvSmem - 1024 - ring) / kStage);
     return n < kKvMaxStages ? n : kKvMaxStages;
   }
   static constexpr size_t total() { return ring + (size_t)stages() * kStage + 1024; }
-  static_assert(stages() >= KG, "each group of warps needs a stage");
+  static_assert(NC % RG == 0 && stages() >= KG, "each group of warps needs a stage");
   static_assert(kKvSegs > kKvMaxStages + KG, "descriptors must outlive their stages");
+  static_assert(kJoin >= kThreads * 6, "the partial results are joined there too");
 };
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -174,6 +177,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ uint32_t minus_1152(uint32_t w) {
   uint32_t r;
   asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(w), "r"(0x64806480u));
+  return r;
+}
+
+// A transposed 8x8 block of fp16: lane 4 r + c holds (r, 2 c), (r, 2 c + 1).
+__device__ __forceinline__ uint32_t transpose8(uint32_t w) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
   return r;
 }
 
@@ -241,14 +251,13 @@ __device__ __forceinline__ KvTile kv_tile(const KvAttnArgs& a, const KvPlan& pl,
   return k;
 }
 
-template <int FMT, int DP, int MT, bool MULTI>
-__global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
+template <int FMT, int DP, int NT, int RG, bool MULTI>
+__global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap map_k,
                    const __grid_constant__ CUtensorMap map_v, const KvAttnArgs a,
                    const KvPlan pl) {
-  using L = KvLayout<DP, MT, MULTI>;
-  constexpr int KG = L::KG, NC = L::NC;
-  constexpr int M = 16 * MT;
+  using L = KvLayout<DP, NT, RG, MULTI>;
+  constexpr int KG = L::KG, NC = L::NC, M = L::M;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
   int bits = 0;
 
   // ---- the split: units before each thread's row tiles, then this CTA's share
-  const int64_t per = (nrt + L::NT - 1) / L::NT;
+  const int64_t per = (nrt + L::kThreads - 1) / L::kThreads;
   const int64_t rt0 = tid * per < nrt ? tid * per : nrt;
   const int64_t rt1 = rt0 + per < nrt ? rt0 + per : nrt;
   long long mine = 0;
@@ -296,19 +305,19 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
   if (lane == 31) s_warp[warp] = incl;
   if (tid < ns) {
     mbar_init(&full[tid], 1);
-    mbar_init(&empty[tid], MT * L::NH);
+    mbar_init(&empty[tid], RG);
     fence_mbar_init();
   }
   if (tid == 0) *s_abort = 0;
   if (tid < kKvProducers) s_tot[tid] = tid ? ~0ull : 0ull;
   if (MULTI)  // rows between and behind a unit's pages hold no key
-    for (int i = tid; i < kKvMaxStages * L::kPages; i += L::NT) {
+    for (int i = tid; i < kKvMaxStages * L::kPages; i += L::kThreads) {
       pages[i] = KvPage{0.f, 0.f, 0.f, 0.f};
       poss[i] = INT32_MAX;
     }
   __syncthreads();
   long long before = 0, total = 0;
-  for (int w = 0; w < L::NT / 32; ++w) {
+  for (int w = 0; w < L::kThreads / 32; ++w) {
     if (w < warp) before += s_warp[w];
     total += s_warp[w];
   }
@@ -606,14 +615,16 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
 
   // ===================================================================== consumers
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kConsumerRegs));
-  const int mt = warp % MT, half = (warp / MT) % L::NH, kg = warp / (MT * L::NH);
-  const int g8 = lane >> 2, c4 = lane & 3;  // row and column quad of a fragment
+  const int rg = warp % RG, kg = warp / RG;
+  const int g8 = lane >> 2, c4 = lane & 3;  // row and column pair of a fragment
+  // Row i of an 8-key block is this key (with 128-byte rows, such that the two
+  // rows of a quarter warp's load differ in the swizzle's high bit).
   constexpr bool PERM = DP >= 128;
-  // the key of column 2 c4 + e of an 8-key block, and the row that lane group n takes
-  auto key_of = [&](int e) { return PERM ? c4 + 4 * e : 2 * c4 + e; };
-  const int krow = PERM ? (g8 >> 1) + 4 * (g8 & 1) : g8;
+  auto key_of = [](int i) { return PERM ? (i >> 1) + 4 * (i & 1) : i; };
+  const int krow = key_of(g8);
+  const int r0 = rg * L::WR;  // the warp's first query row
   float* s_m = reinterpret_cast<float*>(smem + L::ml);
-  float* s_l = s_m + NC * 16;
+  float* s_l = s_m + NC * L::WR;
   float* s_qf = reinterpret_cast<float*>(smem + L::rows);
   int* s_lims = reinterpret_cast<int*>(s_qf + 64);
   float* s_rowm = reinterpret_cast<float*>(s_lims + 128);  // the joined rows' m and l
@@ -621,7 +632,16 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
   unsigned char* s_q = smem + L::q;
   float* s_join = reinterpret_cast<float*>(smem + L::join);
   int slot = kg, phase = 0;
-  bool ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot], phase, s_abort, a.status));
+  // Waits for this group's next stage.  A stage goes to another group on the
+  // next pass when the stages are no multiple of the groups, and copies land
+  // out of order: the pass before must have been used up (its stage released)
+  // before the one bit of the full barrier's phase can mean this pass.
+  auto await = [&]() {
+    const bool got = mbar_wait_bounded(&empty[slot], phase ^ 1, s_abort, a.status) &&
+                     mbar_wait_bounded(&full[slot], phase, s_abort, a.status);
+    return __all_sync(0xFFFFFFFFu, got) != 0;
+  };
+  bool ok = await();
   int cur = ok ? meta[slot * 4] : INT32_MAX;
 
   // queries of a segment: a warp per row, loaded while the one before it is
@@ -685,27 +705,19 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
     int* s_lim = s_lims + (s & 1) * 64;  // still read when the next item's is written
     store_q(s_lim);
     group_sync(NC * 32);
-    const int row0 = mt * 16 + g8;
-    const float qf0 = s_qf[row0], qf1 = s_qf[row0 + 8];
-    const int lim0 = s_lim[row0], lim1 = s_lim[row0 + 8];
-    // operand of k step i (16 dims) of 64-dim half h: dims 64 h + 16 c4 + 4 i ..
-    auto load_q2 = [&](int hi2, uint32_t (&x)[4], uint32_t (&y)[4]) {
-      // two steps at once: hi2 = (64-dim half) * 2 + pair
-      const unsigned char* p0 =
-          s_q + row0 * L::kQPitch + (hi2 >> 1) * 128 + c4 * 32 + (hi2 & 1) * 16;
-      const uint4 u0 = *reinterpret_cast<const uint4*>(p0);
-      const uint4 u1 = *reinterpret_cast<const uint4*>(p0 + 8 * L::kQPitch);
-      x[0] = u0.x; x[2] = u0.y; y[0] = u0.z; y[2] = u0.w;
-      x[1] = u1.x; x[3] = u1.y; y[1] = u1.z; y[3] = u1.w;
-    };
-    float oacc[L::OC / 16][2][4];
+    float oacc[DP / 16][NT][4];
 #pragma unroll
-    for (int j = 0; j < L::OC / 16; ++j)
+    for (int j = 0; j < DP / 16; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) oacc[j][e][k] = 0.f;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int x = 0; x < 4; ++x) oacc[j][n][x] = 0.f;
+    float m[NT][2], l[NT][2];  // of rows r0 + 8 n + 2 c4 + e; l over this lane's keys
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
 
     // One stage; FULL: no row that sees any key misses one of these.
     auto unit = [&](auto full_tag) {
@@ -713,203 +725,209 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
       const unsigned char* kb_ = ring + (size_t)slot * L::kStage;
       const uint32_t vb_ = smem_u32(kb_) + kKvUnit * DP;
       const int nk = is_full ? kKvUnit : meta[slot * 4 + 2];
-      // ---- scores
-      float sc[4][4];
+      // Position of key j of the unit, INT32_MAX if it is none.
+      auto pos_of = [&](int j) {
+        return MULTI ? poss[slot * L::kPages + (MULTI ? j : 0)] : (j < nk ? poss[slot] + j : INT32_MAX);
+      };
+      // ---- scores, keys x rows: block t holds keys 16 t + krow (x = 0, 1) and
+      // 8 further on (x = 2, 3), rows 8 n + 2 c4 + (x & 1).  One row block is
+      // two chains of products for each key block.
+      constexpr int CH = NT == 1 ? 2 : 1;
+      float sc[CH][2][NT][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int c = 0; c < CH; ++c)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) sc[k][x] = 0.f;
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[c][t][n][x] = 0.f;
 #pragma unroll 1
       for (int h = 0; h < DP / 64; ++h) {
-        uint4 w[4];
+        uint4 w[2][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = k * 8 + krow;
-          const int chunk = DP == 64 ? (c4 ^ ((row >> 1) & 3)) : (((h & 1) * 4 + c4) ^ (row & 7));
-          w[k] = *reinterpret_cast<const uint4*>(
-              kb_ + (DP == 256 ? (h >> 1) * kKvUnit * 128 : 0) + row * L::RB + chunk * 16);
-        }
-        // four keys' products side by side: each waits for its own last one only
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int row = t * 16 + e * 8 + krow;
+            const int chunk = DP == 64 ? (c4 ^ ((row >> 1) & 3)) : (((h & 1) * 4 + c4) ^ (row & 7));
+            w[t][e] = *reinterpret_cast<const uint4*>(
+                kb_ + (DP == 256 ? (h >> 1) * kKvUnit * 128 : 0) + row * L::RB + chunk * 16);
+          }
 #pragma unroll
         for (int i2 = 0; i2 < 2; ++i2) {
-          uint32_t q4[2][4];
-          load_q2(2 * h + i2, q4[0], q4[1]);
+          // dims 64 h + 16 c4 + 8 i2 .. + 7 of the rows: two steps' operands
+          uint4 qb[NT];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            qb[n] = *reinterpret_cast<const uint4*>(s_q + (r0 + n * 8 + g8) * L::kQPitch + h * 128 +
+                                                    c4 * 32 + i2 * 16);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t b0, b1;
-              codes4<FMT, false>(i2 ? (i ? w[k].w : w[k].z) : (i ? w[k].y : w[k].x), b0, b1);
-              mma_f16(sc[k], q4[i], b0, b1);
+            for (int t = 0; t < 2; ++t) {
+              uint32_t ka[4];
+              codes4<FMT, false>(i2 ? (i ? w[t][0].w : w[t][0].z) : (i ? w[t][0].y : w[t][0].x), ka[0], ka[2]);
+              codes4<FMT, false>(i2 ? (i ? w[t][1].w : w[t][1].z) : (i ? w[t][1].y : w[t][1].x), ka[1], ka[3]);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma_f16(sc[CH == 2 ? i : 0][t][n], ka, i ? qb[n].z : qb[n].x, i ? qb[n].w : qb[n].y);
             }
         }
       }
+      if (CH == 2) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[0][t][0][x] += sc[CH - 1][t][0][x];
+      }
       // ---- scales, masks, running maximum
-      float iv[MULTI ? 8 : 1], rest[MULTI ? 8 : 1];
-      int pos[MULTI ? 8 : 1];
-      bool tiny = false;
-      if (MULTI) {
+      KvPage pg[MULTI ? 4 : 1];  // of keys 16 t + 8 e + krow
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = (i >> 1) * 8 + key_of(i & 1);
-          const KvPage pg = pages[slot * L::kPages + (MULTI ? j : 0)];
-          iv[MULTI ? i : 0] = pg.iv;
-          rest[MULTI ? i : 0] = pg.rest;
-          pos[MULTI ? i : 0] = poss[slot * L::kPages + (MULTI ? j : 0)];
-          float(&x)[4] = sc[i >> 1];
-          x[i & 1] = fmaf(x[i & 1], pg.ks * qf0, pg.lv);
-          x[2 + (i & 1)] = fmaf(x[2 + (i & 1)], pg.ks * qf1, pg.lv);
+      for (int i = 0; i < (MULTI ? 4 : 1); ++i)
+        pg[i] = pages[slot * L::kPages + (MULTI ? i * 8 + krow : 0)];
+      bool up = false;
+      float top[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float2 qf = *reinterpret_cast<const float2*>(s_qf + r0 + n * 8 + 2 * c4);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const KvPage& e = pg[MULTI ? t * 2 + (x >> 1) : 0];
+            sc[0][t][n][x] = fmaf(sc[0][t][n][x], e.ks * ((x & 1) ? qf.y : qf.x), e.lv);
+          }
+        if constexpr (!is_full) {
+          const int2 lim = *reinterpret_cast<const int2*>(s_lim + r0 + n * 8 + 2 * c4);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              if (pos_of(t * 16 + (x >> 1) * 8 + krow) >= ((x & 1) ? lim.y : lim.x))
+                sc[0][t][n][x] = -INFINITY;
         }
-        tiny = true;
-      } else {
-        const KvPage pg = pages[slot];
-        pos[0] = poss[slot];
-        iv[0] = pg.iv;
-        rest[0] = pg.rest;
-        tiny = pg.rest != 1.f;
-        const float f0 = pg.ks * qf0, f1 = pg.ks * qf1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          sc[k][0] = fmaf(sc[k][0], f0, pg.lv);
-          sc[k][1] = fmaf(sc[k][1], f0, pg.lv);
-          sc[k][2] = fmaf(sc[k][2], f1, pg.lv);
-          sc[k][3] = fmaf(sc[k][3], f1, pg.lv);
-        }
-      }
-      if constexpr (!is_full) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int j = (i >> 1) * 8 + key_of(i & 1);
-          const int ps = MULTI ? pos[MULTI ? i : 0] : (j < nk ? pos[0] + j : INT32_MAX);
-          if (ps >= lim0) sc[i >> 1][i & 1] = -INFINITY;
-          if (ps >= lim1) sc[i >> 1][2 + (i & 1)] = -INFINITY;
+        for (int e = 0; e < 2; ++e) {
+          float v = fmaxf(fmaxf(sc[0][0][n][e], sc[0][0][n][2 + e]),
+                          fmaxf(sc[0][1][n][e], sc[0][1][n][2 + e]));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+          top[n][e] = v;
+          up |= v > m[n][e];
         }
       }
-      float x0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      float x1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-      x0 = fmaxf(x0, fmaxf(fmaxf(sc[2][0], sc[2][1]), fmaxf(sc[3][0], sc[3][1])));
-      x1 = fmaxf(x1, fmaxf(fmaxf(sc[2][2], sc[2][3]), fmaxf(sc[3][2], sc[3][3])));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 1));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 1));
-      x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, 2));
-      x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, 2));
-      if (__any_sync(0xFFFFFFFFu, x0 > m0 || x1 > m1)) {
-        const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
-        const float f0 = n0 == -INFINITY ? 1.f : ex2(m0 - n0);
-        const float f1 = n1 == -INFINITY ? 1.f : ex2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
-        l0 *= f0;
-        l1 *= f1;
+      if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
-        for (int j = 0; j < L::OC / 16; ++j)
+        for (int n = 0; n < NT; ++n) {
+          float f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            oacc[j][e][0] *= f0;
-            oacc[j][e][1] *= f0;
-            oacc[j][e][2] *= f1;
-            oacc[j][e][3] *= f1;
+            const float v = fmaxf(m[n][e], top[n][e]);
+            f[e] = v == -INFINITY ? 1.f : ex2(m[n][e] - v);
+            m[n][e] = v;
+            l[n][e] *= f[e];
           }
-      }
-      const float z0 = m0 == -INFINITY ? 0.f : m0, z1 = m1 == -INFINITY ? 0.f : m1;
-      uint32_t pa[2][4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float p[4];
-        p[0] = ex2(sc[k][0] - z0);
-        p[1] = ex2(sc[k][1] - z0);
-        p[2] = ex2(sc[k][2] - z1);
-        p[3] = ex2(sc[k][3] - z1);
-        l0 = fmaf(p[0], iv[MULTI ? 2 * k : 0], l0);
-        l0 = fmaf(p[1], iv[MULTI ? 2 * k + 1 : 0], l0);
-        l1 = fmaf(p[2], iv[MULTI ? 2 * k : 0], l1);
-        l1 = fmaf(p[3], iv[MULTI ? 2 * k + 1 : 0], l1);
-        if (tiny) {
-          p[0] *= rest[MULTI ? 2 * k : 0];
-          p[1] *= rest[MULTI ? 2 * k + 1 : 0];
-          p[2] *= rest[MULTI ? 2 * k : 0];
-          p[3] *= rest[MULTI ? 2 * k + 1 : 0];
+          for (int j = 0; j < DP / 16; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) oacc[j][n][x] *= f[x & 1];
         }
-        pa[k >> 1][(k & 1) * 2] = pack_f16(p[0], p[1]);
-        pa[k >> 1][(k & 1) * 2 + 1] = pack_f16(p[2], p[3]);
       }
-      // ---- O += P V
-      uint32_t keep[4];  // bytes of this lane's two keys that some row sees
-      if constexpr (!is_full) {
+      // ---- weights, transposed into the second product's operand
+      uint32_t pb[2][NT][2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          keep[k] = 0;
+      for (int n = 0; n < NT; ++n) {
+        const float z0 = m[n][0] == -INFINITY ? 0.f : m[n][0];
+        const float z1 = m[n][1] == -INFINITY ? 0.f : m[n][1];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int j = k * 8 + key_of(e);
-            const int ps = MULTI ? pos[MULTI ? 2 * k + e : 0] : (j < nk ? pos[0] + j : INT32_MAX);
-            if (ps < sg.max_count) keep[k] |= 0xFFFFu << (16 * e);
+            const KvPage& g = pg[MULTI ? t * 2 + e : 0];
+            float p0 = ex2(sc[0][t][n][2 * e] - z0), p1 = ex2(sc[0][t][n][2 * e + 1] - z1);
+            l[n][0] = fmaf(p0, g.iv, l[n][0]);
+            l[n][1] = fmaf(p1, g.iv, l[n][1]);
+            if (MULTI || g.rest != 1.f) {
+              p0 *= g.rest;
+              p1 *= g.rest;
+            }
+            pb[t][n][e] = transpose8(pack_f16(p0, p1));
+          }
+      }
+      // ---- O += V^T P: dims 16 j + 2 g8 (x = 0, 1) and one further (x = 2, 3)
+      const int vrow = key_of(lane & 7);  // lane i of 8 gives the address of row i's key
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        uint32_t keep[2];  // bytes of this lane's keys (2 c4 and the next) that some row sees
+        if constexpr (!is_full) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            keep[e] = 0;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              if (pos_of(t * 16 + e * 8 + key_of(2 * c4 + y)) < sg.max_count)
+                keep[e] |= 0xFFFFu << (16 * y);
           }
         }
-      }
-      const int vrow = PERM ? ((lane & 7) >> 1) + 4 * (lane & 1) : (lane & 7);
-      // lane i of a group of 8 gives the address of matrix row i: the key of
-      // the score's column i
+        const int row = t * 16 + ((lane >> 3) & 1) * 8 + vrow;
 #pragma unroll
-      for (int kk = 0; kk < 2; ++kk) {
-        const int row = kk * 16 + ((lane >> 3) & 1) * 8 + vrow;
-#pragma unroll
-        for (int j2 = 0; j2 < L::OC / 32; ++j2) {
+        for (int j2 = 0; j2 < DP / 32; ++j2) {
           const int ch = j2 * 2 + (lane >> 4);
           const int chunk = DP == 64 ? (ch ^ ((row >> 1) & 3)) : ((ch & 7) ^ (row & 7));
           uint32_t r[4];
-          ldsm4_t(r, vb_ + half * (kKvUnit * 128) + row * L::RB + chunk * 16);
+          ldsm4_t(r, vb_ + (DP == 256 ? (ch >> 3) * kKvUnit * 128 : 0) + row * L::RB + chunk * 16);
           if constexpr (!is_full) {
-            r[0] &= keep[2 * kk];
-            r[1] &= keep[2 * kk + 1];
-            r[2] &= keep[2 * kk];
-            r[3] &= keep[2 * kk + 1];
+            r[0] &= keep[0];
+            r[1] &= keep[1];
+            r[2] &= keep[0];
+            r[3] &= keep[1];
           }
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            uint32_t e0, o0, e1, o1;
-            codes4<FMT, true>(r[2 * x], e0, o0);
-            codes4<FMT, true>(r[2 * x + 1], e1, o1);
+            const int j = j2 * 2 + x;
+            uint32_t va[4];
+            codes4<FMT, true>(r[2 * x], va[0], va[1]);
+            codes4<FMT, true>(r[2 * x + 1], va[2], va[3]);
             if (FMT == kKvE4m3 && !is_full && pl.TT > 1) {
               // Rows of several tokens, and keys that not all of them see: a
               // NaN among those must reach the rows that do, and only them
               // (zero weights do not stop it).
-              auto bad = [](uint32_t w) {
-                return (((w & 0x7FFFu) > 0x7C00u) ? 0xFFFFu : 0u) |
-                       (((w & 0x7FFF0000u) > 0x7C000000u) ? 0xFFFF0000u : 0u);
-              };
-              const uint32_t be0 = bad(e0), be1 = bad(e1), bo0 = bad(o0), bo1 = bad(o1);
-              if (__any_sync(0xFFFFFFFFu, (be0 | be1 | bo0 | bo1) != 0)) {
-                uint32_t see[4];
+              uint32_t bad[4];
+              bool any = false;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {  // 1 where the row sees the key
-                  const int k = 2 * kk + (y >> 1);
-                  const int lim = (y & 1) ? lim1 : lim0;
-                  see[y] = 0;
-#pragma unroll
-                  for (int e = 0; e < 2; ++e) {
-                    const int jj = k * 8 + key_of(e);
-                    const int ps =
-                        MULTI ? pos[MULTI ? 2 * k + e : 0] : (jj < nk ? pos[0] + jj : INT32_MAX);
-                    if (ps < lim) see[y] |= 0x3C00u << (16 * e);
-                  }
-                }
-                float te[4] = {0.f, 0.f, 0.f, 0.f}, to[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(te, see, be0 & 0x3C003C00u, be1 & 0x3C003C00u);
-                mma_f16(to, see, bo0 & 0x3C003C00u, bo1 & 0x3C003C00u);
+              for (int y = 0; y < 4; ++y) {
+                bad[y] = (((va[y] & 0x7FFFu) > 0x7C00u) ? 0xFFFFu : 0u) |
+                         (((va[y] & 0x7FFF0000u) > 0x7C000000u) ? 0xFFFF0000u : 0u);
+                any |= bad[y] != 0;
+              }
+              if (__any_sync(0xFFFFFFFFu, any)) {
+                uint32_t ones[4];
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                  if (te[y] > 0.f) oacc[j2 * 2 + x][0][y] = __int_as_float(0x7FC00000);
-                  if (to[y] > 0.f) oacc[j2 * 2 + x][1][y] = __int_as_float(0x7FC00000);
+                  ones[y] = bad[y] & 0x3C003C00u;
+                  va[y] &= ~bad[y];
                 }
-                e0 &= ~be0;
-                e1 &= ~be1;
-                o0 &= ~bo0;
-                o1 &= ~bo1;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                  const int lim = s_lim[r0 + n * 8 + g8];
+                  uint32_t see[2] = {0u, 0u};  // 1 where the row sees the key
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                      if (pos_of(t * 16 + e * 8 + key_of(2 * c4 + y)) < lim) see[e] |= 0x3C00u << (16 * y);
+                  float hit[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma_f16(hit, ones, see[0], see[1]);
+#pragma unroll
+                  for (int y = 0; y < 4; ++y)
+                    if (hit[y] > 0.f) oacc[j][n][y] = __int_as_float(0x7FC00000);
+                }
               }
             }
-            mma_f16(oacc[j2 * 2 + x][0], pa[kk], e0, e1);
-            mma_f16(oacc[j2 * 2 + x][1], pa[kk], o0, o1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_f16(oacc[j][n], va, pb[t][n][0], pb[t][n][1]);
           }
         }
       }
@@ -924,32 +942,26 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
         slot -= ns;
         phase ^= 1;
       }
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&full[slot], phase, s_abort, a.status));
+      ok = await();
       cur = ok ? meta[slot * 4] : INT32_MAX;
     }
 
     // ---- the item's end: join the groups of warps
-    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 1);
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 1);
-    l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, 2);
-    l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, 2);
-    if (c4 == 0) {
-      s_m[warp * 16 + g8] = m0;
-      s_m[warp * 16 + g8 + 8] = m1;
-      s_l[warp * 16 + g8] = l0;
-      s_l[warp * 16 + g8 + 8] = l1;
-    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 4);
+        l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 8);
+        l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], 16);
+        if (g8 == 0) {
+          s_m[warp * L::WR + n * 8 + 2 * c4 + e] = m[n][e];
+          s_l[warp * L::WR + n * 8 + 2 * c4 + e] = l[n][e];
+        }
+      }
     if (tid == 0) s_flag[0] = *s_abort;
     group_sync(NC * 32);
     const bool aborted = s_flag[0] != 0;
-    float mm0 = -INFINITY, mm1 = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < KG; ++k) {
-      mm0 = fmaxf(mm0, s_m[(k * L::NH * MT + mt) * 16 + g8]);
-      mm1 = fmaxf(mm1, s_m[(k * L::NH * MT + mt) * 16 + g8 + 8]);
-    }
-    const float f0 = m0 == -INFINITY ? (l0 == l0 ? 0.f : l0) : ex2(m0 - mm0);
-    const float f1 = m1 == -INFINITY ? (l1 == l1 ? 0.f : l1) : ex2(m1 - mm1);
     const bool part = !(sg.first && sg.last);  // the item is in several CTAs
     float* wslot = pl.ws + (int64_t)(2 * blockIdx.x + (sg.first ? 1 : 0)) * kKvSlot;
     const int nh = G - sg.h0 % G < pl.GG ? G - sg.h0 % G : pl.GG;
@@ -970,53 +982,65 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
     auto own_factor = [&](float mk, float lk, float m) {  // 0 for no keys, NaN stays
       return mk == -INFINITY ? (lk == lk ? 0.f : lk) : ex2(mk - m);
     };
+    auto entry = [&](int k, int row) {  // the row's place in group k
+      return (k * RG + row / L::WR) * L::WR + row % L::WR;
+    };
     if (tid < sg.nrow && !aborted) {
-      const int rm = tid & 15, rg = tid >> 4;
-      float m = -INFINITY, l = 0.f;
+      float rm = -INFINITY, rl = 0.f;
 #pragma unroll
-      for (int k = 0; k < KG; ++k) m = fmaxf(m, s_m[(k * L::NH * MT + rg) * 16 + rm]);
+      for (int k = 0; k < KG; ++k) rm = fmaxf(rm, s_m[entry(k, tid)]);
 #pragma unroll
       for (int k = 0; k < KG; ++k) {
-        const float mk = s_m[(k * L::NH * MT + rg) * 16 + rm], lk = s_l[(k * L::NH * MT + rg) * 16 + rm];
-        l = fmaf(mk == -INFINITY ? (lk == lk ? 0.f : 1.f) : lk, own_factor(mk, lk, m), l);
+        const float mk = s_m[entry(k, tid)], lk = s_l[entry(k, tid)];
+        rl = fmaf(mk == -INFINITY ? (lk == lk ? 0.f : 1.f) : lk, own_factor(mk, lk, rm), rl);
       }
       const bool none = s_lim[tid] == 0;  // padding: whatever its query gave
-      s_rowm[tid] = none ? -INFINITY : m;
-      s_rowl[tid] = none ? 0.f : l;
+      s_rowm[tid] = none ? -INFINITY : rm;
+      s_rowl[tid] = none ? 0.f : rl;
     }
+    float f[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float mm = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) mm = fmaxf(mm, s_m[entry(k, r0 + n * 8 + 2 * c4 + e)]);
+        f[n][e] = own_factor(m[n][e], l[n][e], mm);
+      }
     // The accumulators go through shared memory, as many columns at a time as
     // its room holds of the rows in use.
-    const int rr = sg.nrow < 16 ? sg.nrow : 16;
-    int per = rr <= 4 ? 4 : (rr <= 8 ? 2 : 1);
-    per = per < L::OC / 32 ? per : L::OC / 32;
+    const int rr = sg.nrow < L::WR ? sg.nrow : L::WR;
+    int per = 1;
+    while (per * 2 <= DP / 32 && NC * rr * (per * 64 + 4) <= L::kJoin) per *= 2;
     const int jp = per * 32 + 4;
 #pragma unroll
-    for (int cb = 0; cb < L::OC / 32; ++cb) {
+    for (int cb = 0; cb < DP / 32; ++cb) {
       const int sub = cb & (per - 1);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const auto& o = oacc[cb * 2 + j];
-        float* d = s_join + (warp * rr + g8) * jp + sub * 32 + j * 16 + c4 * 4;
-        if (g8 < rr)
-          *reinterpret_cast<float4*>(d) =
-              make_float4(o[0][0] * f0, o[1][0] * f0, o[0][1] * f0, o[1][1] * f0);
-        if (g8 + 8 < rr)
-          *reinterpret_cast<float4*>(d + 8 * jp) =
-              make_float4(o[0][2] * f1, o[1][2] * f1, o[0][3] * f1, o[1][3] * f1);
-      }
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const auto& o = oacc[cb * 2 + j][n];
+          const int row = n * 8 + 2 * c4;
+          float* d = s_join + (warp * rr + row) * jp + sub * 32 + j * 16 + 2 * g8;
+          if (row < rr) *reinterpret_cast<float2*>(d) = make_float2(o[0] * f[n][0], o[2] * f[n][0]);
+          if (row + 1 < rr)
+            *reinterpret_cast<float2*>(d + jp) = make_float2(o[1] * f[n][1], o[3] * f[n][1]);
+        }
       if (sub != per - 1) continue;
       group_sync(NC * 32);
       const int pieces = per * 8;  // of four columns
-      for (int i = tid; i < sg.nrow * L::NH * pieces && !aborted; i += NC * 32) {
-        const int row = i / (L::NH * pieces), rem = i - row * (L::NH * pieces);
-        const int hf = rem / pieces, pc = rem - hf * pieces;
-        const int oc = hf * L::OC + (cb - sub) * 32 + pc * 4;  // the output column
+      for (int i = tid; i < sg.nrow * pieces && !aborted; i += NC * 32) {
+        const int row = i / pieces, pc = i - row * pieces;
+        const int oc = (cb - sub) * 32 + pc * 4;  // the output column
         if (oc >= a.D) continue;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int k = 0; k < KG; ++k) {
-          const int w = (k * L::NH + hf) * MT + (row >> 4);
-          const float4 u = *reinterpret_cast<const float4*>(s_join + (w * rr + (row & 15)) * jp + pc * 4);
+          const int w = k * RG + row / L::WR;
+          const float4 u =
+              *reinterpret_cast<const float4*>(s_join + (w * rr + row % L::WR) * jp + pc * 4);
           o.x += u.x;
           o.y += u.y;
           o.z += u.z;
@@ -1032,7 +1056,7 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
           finish(row, oc, s_rowm[row], s_rowl[row], o);
         }
       }
-      if (cb != L::OC / 32 - 1) group_sync(NC * 32);
+      if (cb != DP / 32 - 1) group_sync(NC * 32);
     }
     if (ok && s + 1 < nseg) load_q(segs[(s + 1) % kKvSegs]);
     if (part && !aborted) {
@@ -1115,36 +1139,39 @@ __global__ void __launch_bounds__(KvLayout<DP, MT, MULTI>::NT, 1)
   }
 }
 
+// nt, rg: 1, 1 / 2, 1 / 2, 2 / 2, 4.
 template <int DP>
 cudaError_t launch_kv_attn_dp(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& a,
-                              KvPlan pl, int mt, int grid, cudaStream_t stream);
+                              KvPlan pl, int nt, int rg, int grid, cudaStream_t stream);
 
 #ifdef IDX_KV_ATTN_DP
-template <int FMT, int DP, int MT, bool MULTI>
+template <int FMT, int DP, int NT, int RG, bool MULTI>
 static cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& a,
                               KvPlan& pl, int grid, cudaStream_t stream) {
-  using L = KvLayout<DP, MT, MULTI>;
+  using L = KvLayout<DP, NT, RG, MULTI>;
   pl.nstage = L::stages();
   const size_t smem = L::total();
-  auto kern = kv_attn_kernel<FMT, DP, MT, MULTI>;
+  auto kern = kv_attn_kernel<FMT, DP, NT, RG, MULTI>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kern<<<grid, L::NT, smem, stream>>>(mk, mv, a, pl);
+  kern<<<grid, L::kThreads, smem, stream>>>(mk, mv, a, pl);
   return cudaGetLastError();
 }
 
 template <>
 cudaError_t launch_kv_attn_dp<IDX_KV_ATTN_DP>(const CUtensorMap& mk, const CUtensorMap& mv,
-                                              const KvAttnArgs& a, KvPlan pl, int mt, int grid,
-                                              cudaStream_t stream) {
+                                              const KvAttnArgs& a, KvPlan pl, int nt, int rg,
+                                              int grid, cudaStream_t stream) {
   constexpr int DP = IDX_KV_ATTN_DP;
   const bool multi = pl.ppt > 1;
-#define IDX_KV_GO(F, M)                                                            \
-  (multi ? launch_one<F, DP, M, true>(mk, mv, a, pl, grid, stream)                 \
-         : launch_one<F, DP, M, false>(mk, mv, a, pl, grid, stream))
-  if (a.format == kKvE4m3)
-    return mt == 1 ? IDX_KV_GO(kKvE4m3, 1) : mt == 2 ? IDX_KV_GO(kKvE4m3, 2) : IDX_KV_GO(kKvE4m3, 4);
-  return mt == 1 ? IDX_KV_GO(kKvInt8, 1) : mt == 2 ? IDX_KV_GO(kKvInt8, 2) : IDX_KV_GO(kKvInt8, 4);
+#define IDX_KV_GO(F, N, R)                                                         \
+  (multi ? launch_one<F, DP, N, R, true>(mk, mv, a, pl, grid, stream)              \
+         : launch_one<F, DP, N, R, false>(mk, mv, a, pl, grid, stream))
+#define IDX_KV_ROWS(F)                                                             \
+  (nt == 1 ? IDX_KV_GO(F, 1, 1)                                                    \
+           : rg == 1 ? IDX_KV_GO(F, 2, 1) : rg == 2 ? IDX_KV_GO(F, 2, 2) : IDX_KV_GO(F, 2, 4))
+  return a.format == kKvE4m3 ? IDX_KV_ROWS(kKvE4m3) : IDX_KV_ROWS(kKvInt8);
+#undef IDX_KV_ROWS
 #undef IDX_KV_GO
 }
 #endif
