@@ -321,9 +321,8 @@ KV_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 
 
-def _kv_tensor(ctx, name, t, dtypes, shape, contiguous=True):
-    """t, checked: on the context's device, of one of the dtypes and of the shape
-    (None: any size)."""
+def _kv_refuse(ctx, name, t, dtypes, shape, contiguous):
+    """Says what is wrong with a tensor (nothing: returns)."""
     dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     if t.device.type != "cuda" or t.device.index != ctx.device:
         raise ValueError("%s must be on cuda:%d" % (name, ctx.device))
@@ -333,32 +332,72 @@ def _kv_tensor(ctx, name, t, dtypes, shape, contiguous=True):
         raise ValueError("%s must be of shape %s" % (name, tuple("*" if n is None else n for n in shape)))
     if contiguous and not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
-    return t
+
+
+def _kv_tensor(ctx, name, t, dtype, shape):
+    """The address of t, a contiguous tensor of this dtype and shape on the context's device.
+    (A call checks ten tensors: the one comparison here is what it costs, the reasons come from
+    _kv_refuse.)"""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != ctx.device or not t.is_contiguous():
+        _kv_refuse(ctx, name, t, dtype, shape, True)
+    return t.data_ptr()
 
 
 def _kv_rows(name, t, lead):
     """The row stride of t [..rows][heads][D] whose rows are contiguous and evenly spaced."""
-    heads, D = t.shape[-2:]
-    if t.stride(-1) != 1 or (heads > 1 and t.stride(-2) != D):
+    shape = t.shape
+    heads, D = shape[-2:]
+    if t.is_contiguous():
+        return heads * D
+    stride = t.stride()
+    if stride[-1] != 1 or (heads > 1 and stride[-2] != D):
         raise ValueError("%s's rows must be contiguous" % name)
-    ld = None
+    ld, below = None, 1
     for d in range(lead - 1, -1, -1):  # dimensions of one row tell nothing
-        if t.shape[d] > 1:
-            below = 1
-            for n in t.shape[d + 1:lead]:
-                below *= n
-            if t.stride(d) % below or ld not in (None, t.stride(d) // below):
+        if shape[d] > 1:
+            if stride[d] % below or ld not in (None, stride[d] // below):
                 raise ValueError("%s's rows must be evenly spaced" % name)
-            ld = t.stride(d) // below
+            ld = stride[d] // below
+        below *= shape[d]
     return heads * D if ld is None else ld
 
 
+def _kv_bf16(ctx, name, t, shape, lead):
+    """Address and row stride of bf16 rows [..lead dims][heads][D]."""
+    if t.dtype not in _BF16 or t.shape != shape or t.get_device() != ctx.device:
+        _kv_refuse(ctx, name, t, _BF16, shape, False)
+    return t.data_ptr(), _kv_rows(name, t, lead)
+
+
 def _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale):
-    _kv_tensor(ctx, "k_cache", k_cache, tuple(KV_FORMATS), (None,) * 4)
-    _kv_tensor(ctx, "v_cache", v_cache, k_cache.dtype, k_cache.shape)
-    _kv_tensor(ctx, "k_scale", k_scale, torch.float32, k_cache.shape[:2])
-    _kv_tensor(ctx, "v_scale", v_scale, torch.float32, k_cache.shape[:2])
-    return (*k_cache.shape, KV_FORMATS[k_cache.dtype])
+    fmt = KV_FORMATS.get(k_cache.dtype)
+    if fmt is None or k_cache.dim() != 4:
+        _kv_refuse(ctx, "k_cache", k_cache, tuple(KV_FORMATS), (None,) * 4, True)
+    shape = k_cache.shape
+    per = shape[:2]
+    return (shape, fmt, _kv_tensor(ctx, "k_cache", k_cache, k_cache.dtype, shape),
+            _kv_tensor(ctx, "v_cache", v_cache, k_cache.dtype, shape),
+            _kv_tensor(ctx, "k_scale", k_scale, torch.float32, per),
+            _kv_tensor(ctx, "v_scale", v_scale, torch.float32, per))
+
+
+def _kv_table(ctx, page_table, B):
+    """Address, width and row stride of an int32 [B][N] table of contiguous rows."""
+    shape = page_table.shape
+    if page_table.dtype != torch.int32 or len(shape) != 2 or shape[0] != B \
+            or page_table.get_device() != ctx.device:
+        _kv_refuse(ctx, "page_table", page_table, torch.int32, (B, None), False)
+    N = shape[1]
+    ld, one = page_table.stride()
+    if (N > 1 and one != 1) or (B > 1 and ld < N):
+        raise ValueError("page_table's rows must be contiguous")
+    return page_table.data_ptr(), N, ld if B > 1 else N
+
+
+def _kv_stream(ctx, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(ctx.device)
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
 def kv_block_tables(ctx, cached, fresh, P, n_blocks, page_table, free_list, free_head,
@@ -368,39 +407,35 @@ def kv_block_tables(ctx, cached, fresh, P, n_blocks, page_table, free_list, free
     page_counts [B][T] of the new tokens; free_head_out[0] (may be None) = the entry after the
     last one taken.  All tensors int32."""
     i32 = torch.int32
-    _kv_tensor(ctx, "slots", slots, i32, (None, None))
-    B, T = slots.shape
-    _kv_tensor(ctx, "cached", cached, i32, (B,))
-    _kv_tensor(ctx, "page_table", page_table, i32, (B, None), contiguous=False)
-    if page_table.stride(1) != 1 or (B > 1 and page_table.stride(0) < page_table.shape[1]):
-        raise ValueError("page_table's rows must be contiguous")
-    _kv_tensor(ctx, "free_list", free_list, i32, (None,))
-    for name, t, shape in (("fresh", fresh, (B,)), ("free_head", free_head, (1,)),
-                           ("free_head_out", free_head_out, (1,)),
-                           ("key_counts", key_counts, (B, T)), ("page_counts", page_counts, (B, T))):
-        if t is not None or name in ("key_counts", "page_counts"):
-            _kv_tensor(ctx, name, t, i32, shape)
-    N = page_table.shape[1]
-    _check(lib().kv_block_tables(ctx.handle, _ptr(cached), _ptr(fresh), B, T, P, N,
-                                 _ptr(page_table), page_table.stride(0) if B > 1 else N, n_blocks,
-                                 _ptr(free_list), free_list.numel(), _ptr(free_head),
-                                 _ptr(free_head_out), _ptr(slots), _ptr(key_counts),
-                                 _ptr(page_counts), _stream(stream, slots.device)),
-           "kv_block_tables")
+    shape = slots.shape
+    if len(shape) != 2:
+        _kv_refuse(ctx, "slots", slots, i32, (None, None), True)
+    B, T = shape
+    table, N, ld = _kv_table(ctx, page_table, B)
+    n_free = free_list.numel()
+    _check(lib().kv_block_tables(
+        ctx.handle, _kv_tensor(ctx, "cached", cached, i32, (B,)),
+        None if fresh is None else _kv_tensor(ctx, "fresh", fresh, i32, (B,)), B, T, P, N, table,
+        ld, n_blocks, _kv_tensor(ctx, "free_list", free_list, i32, (n_free,)), n_free,
+        None if free_head is None else _kv_tensor(ctx, "free_head", free_head, i32, (1,)),
+        None if free_head_out is None else _kv_tensor(ctx, "free_head_out", free_head_out, i32, (1,)),
+        _kv_tensor(ctx, "slots", slots, i32, shape),
+        _kv_tensor(ctx, "key_counts", key_counts, i32, shape),
+        _kv_tensor(ctx, "page_counts", page_counts, i32, shape), _kv_stream(ctx, stream)),
+        "kv_block_tables")
     return slots, key_counts, page_counts
 
 
 def kv_append(ctx, k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
     """Rows k, v (bf16 [R][H][D], rows may be strided) into the cache's slots[r] (int32 [R], or any
     shape of R elements; -1: none), with the scales of the pages they reach."""
-    n_blocks, H, P, D, fmt = _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale)
+    (n_blocks, H, P, D), fmt, kc, vc, ks, vs = _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale)
     R = slots.numel()
-    _kv_tensor(ctx, "slots", slots, torch.int32, slots.shape)
-    _kv_tensor(ctx, "k", k, _BF16, (R, H, D), contiguous=False)
-    _kv_tensor(ctx, "v", v, _BF16, (R, H, D), contiguous=False)
-    _check(lib().kv_append(ctx.handle, _ptr(k), _ptr(v), _kv_rows("k", k, 1), _kv_rows("v", v, 1),
-                           _ptr(slots), R, H, D, P, n_blocks, fmt, _ptr(k_cache), _ptr(v_cache),
-                           _ptr(k_scale), _ptr(v_scale), _stream(stream, k.device)), "kv_append")
+    k_at, ldk = _kv_bf16(ctx, "k", k, (R, H, D), 1)
+    v_at, ldv = _kv_bf16(ctx, "v", v, (R, H, D), 1)
+    _check(lib().kv_append(ctx.handle, k_at, v_at, ldk, ldv,
+                           _kv_tensor(ctx, "slots", slots, torch.int32, slots.shape), R, H, D, P,
+                           n_blocks, fmt, kc, vc, ks, vs, _kv_stream(ctx, stream)), "kv_append")
 
 
 def kv_attention(ctx, q, k_cache, v_cache, k_scale, v_scale, page_table, key_counts, out, lse=None,
@@ -408,30 +443,27 @@ def kv_attention(ctx, q, k_cache, v_cache, k_scale, v_scale, page_table, key_cou
     """out (bf16 [B][T][Q][D]) = attention of q (bf16 [B][T][Q][D], rows may be strided) over the
     first key_counts[b, t] keys of the request: of the pages page_idx[b*T+t] (int32 [B*T][K], -1:
     none), or of all its pages.  lse: fp32 [B][T][Q] or None; scale: 1/sqrt(D) if None."""
-    n_blocks, H, P, D, fmt = _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale)
-    _kv_tensor(ctx, "q", q, _BF16, (None, None, None, D), contiguous=False)
-    B, T, Q, _ = q.shape
-    _kv_tensor(ctx, "out", out, _BF16, (B, T, Q, D))
-    _kv_tensor(ctx, "page_table", page_table, torch.int32, (B, None), contiguous=False)
-    if page_table.stride(1) != 1 or (B > 1 and page_table.stride(0) < page_table.shape[1]):
-        raise ValueError("page_table's rows must be contiguous")
-    N = page_table.shape[1]
+    (n_blocks, H, P, D), fmt, kc, vc, ks, vs = _kv_cache(ctx, k_cache, v_cache, k_scale, v_scale)
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != D:
+        _kv_refuse(ctx, "q", q, _BF16, (None, None, None, D), False)
+    B, T, Q, _ = shape
+    q_at, ldq = _kv_bf16(ctx, "q", q, shape, 2)
+    if out.dtype not in _BF16:
+        _kv_refuse(ctx, "out", out, _BF16, shape, True)
+    table, N, ld = _kv_table(ctx, page_table, B)
     if key_counts.numel() != B * T:
         raise ValueError("key_counts must have B*T elements")
-    _kv_tensor(ctx, "key_counts", key_counts, torch.int32, key_counts.shape)
-    if lse is not None:
-        _kv_tensor(ctx, "lse", lse, torch.float32, (B, T, Q))
-    K = 0
+    K, idx = 0, None
     if page_idx is not None:
-        _kv_tensor(ctx, "page_idx", page_idx, torch.int32, (B * T, None))
+        if page_idx.dim() != 2 or page_idx.shape[1] == 0:
+            raise ValueError("page_idx must be int32 [B*T][K] with K > 0")
         K = page_idx.shape[1]
-        if K == 0:
-            raise ValueError("page_idx must have a column")
-    if scale is None:
-        scale = D ** -0.5
-    _check(lib().kv_attention(ctx.handle, _ptr(q), _kv_rows("q", q, 2), _ptr(k_cache),
-                              _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), n_blocks, fmt,
-                              _ptr(page_table), page_table.stride(0) if B > 1 else N, N,
-                              _ptr(key_counts), _ptr(page_idx), K, B, T, Q, H, D, P, scale,
-                              _ptr(out), _ptr(lse), _stream(stream, q.device)), "kv_attention")
+        idx = _kv_tensor(ctx, "page_idx", page_idx, torch.int32, (B * T, K))
+    _check(lib().kv_attention(
+        ctx.handle, q_at, ldq, kc, vc, ks, vs, n_blocks, fmt, table, ld, N,
+        _kv_tensor(ctx, "key_counts", key_counts, torch.int32, key_counts.shape), idx, K, B, T, Q,
+        H, D, P, D ** -0.5 if scale is None else scale, _kv_tensor(ctx, "out", out, out.dtype, shape),
+        None if lse is None else _kv_tensor(ctx, "lse", lse, torch.float32, (B, T, Q)),
+        _kv_stream(ctx, stream)), "kv_attention")
     return out, lse
