@@ -1,15 +1,24 @@
 // kv_attn.cu -- what kv_attention launches (the kernels are in kv_attn.cuh).
-#include <cudaTypedefs.h>
-
 #include "kv_attn.cuh"
 
 namespace idx {
 
-PFN_cuTensorMapEncodeTiled_v12000 get_encode();
-
 size_t kv_attn_ws_floats(int num_sms) { return (size_t)num_sms * 2 * kKvSlot; }
 
+bool encode_cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const KvAttnArgs& a,
+                      const uint8_t* cache, int dp, int rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)a.D, (cuuint64_t)a.n_blocks * a.H * a.P};
+  const cuuint64_t strides[1] = {(cuuint64_t)a.D};
+  const cuuint32_t box[2] = {(cuuint32_t)(dp < 128 ? dp : 128), (cuuint32_t)rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(cache), dims, strides, box, estr,
+                CU_TENSOR_MAP_INTERLEAVE_NONE,
+                dp == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int num_sms, cudaStream_t stream) {
+  if (kv_attn_tc_supported(a)) return launch_kv_attn_tc(a, num_sms, stream);
   auto encode = get_encode();
   if (!encode) return cudaErrorNotSupported;
   const int G = a.Q / a.H;
@@ -31,20 +40,10 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int num_sms, cudaStream_t stream
   pl.box = a.P < kKvUnit ? a.P : kKvUnit;
   pl.ws = a.ws;
   pl.arrive = a.arrive;
-  // The cache as rows of D codes; boxes of a unit's rows and at most 128 codes,
-  // 16-byte pieces swizzled within 128 (64) byte rows; codes past D read as 0.
   CUtensorMap mk, mv;
-  const cuuint64_t dims[2] = {(cuuint64_t)a.D, (cuuint64_t)a.n_blocks * a.H * a.P};
-  const cuuint64_t strides[1] = {(cuuint64_t)a.D};
-  const cuuint32_t box[2] = {(cuuint32_t)(dp < 128 ? dp : 128), (cuuint32_t)pl.box};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapSwizzle sw = dp == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
-  for (int i = 0; i < 2; ++i)
-    if (encode(i ? &mv : &mk, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-               const_cast<uint8_t*>(i ? a.v_cache : a.k_cache), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
+  if (!encode_cache_map(encode, &mk, a, a.k_cache, dp, pl.box) ||
+      !encode_cache_map(encode, &mv, a, a.v_cache, dp, pl.box))
+    return cudaErrorInvalidValue;
   if (dp == 64) return launch_kv_attn_dp<64>(mk, mv, a, pl, nt, rg, num_sms, stream);
   if (dp == 128) return launch_kv_attn_dp<128>(mk, mv, a, pl, nt, rg, num_sms, stream);
   return launch_kv_attn_dp<256>(mk, mv, a, pl, nt, rg, num_sms, stream);

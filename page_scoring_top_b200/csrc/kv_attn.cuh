@@ -51,6 +51,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include <type_traits>
 
@@ -78,10 +79,10 @@ struct KvPlan {
   int pitch;        // rows from page to page in a unit of several pages
   int box;          // rows of a copy
   int nstage;
-  float* ws;        // 2 slots per CTA: O [64][256], m [64], l [64]
+  float* ws;        // 2 slots per CTA: O [64][256], m, l
   int32_t* arrive;  // one counter per CTA, zero between launches
 };
-constexpr int kKvSlot = 64 * 256 + 128;  // floats of a workspace slot
+constexpr int kKvSlot = 64 * 256 + 256;  // floats of a workspace slot (also O [128][128], m, l)
 
 struct KvSeg {
   int64_t unit0;    // the item's first unit, as the split counts
@@ -203,6 +204,19 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t& x, uint32_t& y) {
     x = minus_1152(__byte_perm(w, 0x64646464u, ACROSS ? 0x4240 : 0x4140));
     y = minus_1152(__byte_perm(w, 0x64646464u, ACROSS ? 0x4341 : 0x4342));
   }
+}
+
+// A page's entry from its scales.
+__device__ __forceinline__ KvPage kv_scales(float ks, float vs) {
+  const float v1 = fmaxf(vs, kKvMinScale);
+  const uint32_t vb = __float_as_uint(v1);
+  KvPage e;
+  e.ks = ks;
+  // 2^lv must give a power of two back exactly
+  e.lv = (vb & 0x7FFFFFu) ? __log2f(v1) : (float)((int)(vb >> 23) - 127);
+  e.iv = __fdiv_rn(1.f, v1);
+  e.rest = vs < kKvMinScale ? vs * (1.f / kKvMinScale) : (vs == vs ? 1.f : vs);
+  return e;
 }
 
 // Units of row tile rt (at least one: a tile without keys still has an output),
@@ -462,14 +476,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
           int pos = INT32_MAX, row = 0, nk = 0;
           if (valid) {
             const int64_t cell = (int64_t)id * a.H + g;
-            const float vs = __ldg(a.v_scale + cell);
-            const float v1 = fmaxf(vs, kKvMinScale);
-            pg.ks = __ldg(a.k_scale + cell);
-            // 2^lv must give a power of two back exactly
-            const uint32_t vb = __float_as_uint(v1);
-            pg.lv = (vb & 0x7FFFFFu) ? __log2f(v1) : (float)((int)(vb >> 23) - 127);
-            pg.iv = __fdiv_rn(1.f, v1);
-            pg.rest = vs < kKvMinScale ? vs * (1.f / kKvMinScale) : (vs == vs ? 1.f : vs);
+            pg = kv_scales(__ldg(a.k_scale + cell), __ldg(a.v_scale + cell));
             pos = p * a.P + sub;
             row = (int)(cell * a.P) + sub;
             nk = a.P - sub < kKvUnit ? a.P - sub : kKvUnit;
@@ -1140,6 +1147,14 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
 }
 
 // nt, rg: 1, 1 / 2, 1 / 2, 2 / 2, 4.
+PFN_cuTensorMapEncodeTiled_v12000 get_encode();
+// The cache as rows of D codes; boxes of `rows` rows and at most 128 codes,
+// 16-byte pieces swizzled within 128 (dp == 64: 64) bytes; codes past D read as 0.
+bool encode_cache_map(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* map, const KvAttnArgs& a,
+                      const uint8_t* cache, int dp, int rows);
+bool kv_attn_tc_supported(const KvAttnArgs& a);
+cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, int num_sms, cudaStream_t stream);
+
 template <int DP>
 cudaError_t launch_kv_attn_dp(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& a,
                               KvPlan pl, int nt, int rg, int grid, cudaStream_t stream);

@@ -333,6 +333,47 @@ def test_attention_causal_tokens(ctx, T, Q, H):
     check_attn(ctx, attn_case(T + Q, 3, T, Q, H, 128, 16, N, "e4m3", counts))
 
 
+@pytest.mark.parametrize("B,T,Q,H,D,P,pos0,fmt", [
+    (1, 17, 4, 1, 64, 32, 0, "int8"), (1, 33, 4, 1, 128, 64, 0, "e4m3"), (2, 40, 8, 2, 128, 64, 900, "e4m3"),
+    (2, 40, 8, 2, 128, 64, 900, "int8"), (1, 130, 4, 1, 64, 128, 257, "e4m3"), (1, 9, 16, 2, 128, 256, 1000, "int8"),
+    (3, 20, 16, 2, 96, 48, 70, "e4m3"), (1, 33, 8, 1, 112, 7, 50, "int8"), (2, 70, 2, 1, 48, 100, 333, "e4m3"),
+    (1, 20, 256, 1, 128, 32, 90, "e4m3"), (1, 3, 130, 1, 64, 16, 40, "int8"), (1, 16, 8, 1, 128, 1, 30, "e4m3"),
+    (1, 70, 1, 1, 64, 7, 30, "e4m3"), (1, 16, 8, 1, 128, 64, 30000, "e4m3")])
+def test_attention_prompts(ctx, B, T, Q, H, D, P, pos0, fmt):
+    # more than 64 rows (tokens x heads) to a kv head; the last request starts empty
+    counts = np.arange(T)[None] + 1 + np.array([pos0] * (B - 1) + [pos0 if B == 1 else 0])[:, None]
+    N = -(-int(counts.max()) // P)
+    check_attn(ctx, attn_case(T + D + P, B, T, Q, H, D, P, N, fmt, counts))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_prompt_many_tiles_per_sm(ctx, D):
+    counts = np.array([32000, 31000, 32000, 777, 29000, 31999])[:, None] - 15 + np.arange(16)
+    check_attn(ctx, attn_case(28, 6, 16, 8, 1, D, 64, 500, "e4m3", counts))
+
+
+def test_attention_prompt_many_items_per_sm(ctx):
+    rng = np.random.default_rng(29)
+    counts = rng.integers(0, 300, (200, 1)) + np.arange(17)[None]
+    counts[::7] = 0
+    check_attn(ctx, attn_case(29, 200, 17, 4, 1, 64, 32, 10, "int8", counts))
+
+
+def test_attention_prompt_padding_and_scales(ctx):
+    # padded tokens between real ones, a negative softmax scale, value scales far
+    # apart (as in test_attention_scales_far_apart), a block outside the pool
+    rng = np.random.default_rng(30)
+    counts = np.where(rng.random((2, 40)) < 0.3, 0, rng.integers(1, 600, (2, 40)))
+    c = attn_case(30, 2, 40, 4, 1, 128, 64, 10, "e4m3", counts, vexp=30)
+    check_attn(ctx, c)
+    c["scale"] = -c["scale"]
+    check_attn(ctx, c)
+    c = attn_case(31, 1, 40, 4, 1, 64, 32, 10, "int8", 280 + np.arange(40)[None], poison=False)
+    c["table"][0, 3] = -1
+    c["table"][0, 6] = 99999
+    check_attn(ctx, c, bits=4)
+
+
 def test_attention_counts_in_any_order(ctx):
     # key counts are data: neither rising nor equal over a request's tokens
     rng = np.random.default_rng(2)
@@ -411,13 +452,13 @@ def test_attention_large_and_tiny_queries(ctx):
 
 def test_attention_later_nan_stays_out(ctx):
     # a NaN value or key that only the last token sees must not reach the others
-    for T, Q, H in ((4, 4, 1), (16, 8, 1), (40, 4, 1)):
+    for T, Q, H, P in ((4, 4, 1, 16), (16, 8, 1, 16), (40, 4, 1, 16), (40, 4, 1, 32)):
         counts = 50 + np.arange(T)[None] + 1
-        N = -(-(50 + T) // 16)
-        c = attn_case(19, 1, T, Q, H, 64, 16, N, "e4m3", counts)
+        N = -(-(50 + T) // P)
+        c = attn_case(19, 1, T, Q, H, 64, P, N, "e4m3", counts)
         clean = launch_attn(ctx, c)[0]
         for w in ("kc", "vc"):
-            p, i = divmod(50 + T - 1, 16)
+            p, i = divmod(50 + T - 1, P)
             c[w][c["table"][0, p], :, i, 5] = 127
         out = launch_attn(ctx, c)[0]
         assert torch.isnan(out[0, T - 1]).any()
