@@ -12,11 +12,12 @@
 // tensor cores, 1024 of the exponent unit (128 x 128 at 16 a cycle) and, when
 // its keys come from HBM, 1400 of the memory; so the kernel is built to keep
 // all of them busy at once:
-//  * three producer warps: block table look-ups, TMA copies of the codes of K and V
-//    (16 KB each at D = 128) into a ring of four, scales of the tile's keys;
-//  * four converter warps: codes -> fp16 operands (128-byte swizzled; K as K-major,
-//    V as it lies, keys by rows: the B operand in its MN-major form, so nothing
-//    is transposed), two buffers each; queries at an item's start;
+//  * three producer warps: block table look-ups, TMA copies of the codes into a
+//    ring of five 64-key stages for K and one for V, scales of the tile's keys;
+//  * two converter warpgroups, one for K and one for V: codes -> fp16 operands
+//    (128-byte swizzled; K as K-major, one buffer; V as it lies, keys by rows: the
+//    B operand in its MN-major form, so nothing is transposed, two buffers);
+//    the first also writes the queries at an item's start;
 //  * one MMA warp: S of tile n into one of two TMEM buffers, then O += P V of
 //    tile n - 1;
 //  * two softmax warpgroups take alternate tiles, a thread per query row, with
@@ -42,10 +43,12 @@ namespace idx {
 
 namespace {
 
-constexpr int kTkThreads = 512;
+constexpr int kTkThreads = 640;
 constexpr int kTkSoft = 256;       // softmax threads
 constexpr int kTkKeys = 128;       // keys per tile
 constexpr int kTkRows = 128;
+constexpr int kTkHalf = 64;        // keys of a copied stage
+constexpr int kTkStages = 5;       // stages of the rings of K and of V
 constexpr int kTkCharge = 4;       // tiles that an item's start and end count for
 constexpr int kTkMeta = 6;         // tiles whose scales are held: up to five are in the pipeline
 constexpr float kTkSlack = 8.f;    // log2 by which a row may exceed its reference
@@ -53,20 +56,18 @@ constexpr float kTkSlack = 8.f;    // log2 by which a row may exceed its referen
 template <int DP, bool PERKEY>
 struct TkLayout {
   static constexpr int kOp = kTkKeys * DP * 2;        // bytes of a 128-row operand
-  static constexpr int kRaw = kTkKeys * DP;           // bytes of a tile's codes
+  static constexpr int kRaw = kTkHalf * DP;           // bytes of half a tile's codes
   static constexpr int kPer = PERKEY ? kTkKeys : 4;   // scale entries of a tile
-  static constexpr size_t bars = 0;                   // 27 barriers
-  static constexpr size_t misc = 256;                 // 64 ints
+  static constexpr size_t bars = 0;                   // 36 barriers
+  static constexpr size_t misc = 384;                 // 64 ints
   static constexpr size_t rows = misc + 256;          // factor, limit (two items'); m, l of two streams
   static constexpr size_t nanpos = rows + 2 * 128 * 8 + 512 * 4;  // first position of a NaN per column
   static constexpr size_t meta = nanpos + 2 * 128 * 4;
   static constexpr size_t q = (meta + (size_t)kTkMeta * kPer * sizeof(KvPage) + 1023) & ~(size_t)1023;
   static constexpr size_t k16 = q + kOp;
-  static constexpr size_t v16 = k16 + 2 * kOp;
+  static constexpr size_t v16 = k16 + kOp;
   static constexpr size_t raw = v16 + 2 * kOp;
-  // (with an entry per key the ring of codes is what has to give)
-  static constexpr int kStages = (kKvSmem - 1024 - raw) / kRaw >= 4 ? 4 : 3;
-  static constexpr size_t total = raw + (size_t)kStages * kRaw + 1024;
+  static constexpr size_t total = raw + (size_t)2 * kTkStages * kRaw + 1024;
   static_assert(total <= kKvSmem, "shared memory");
 };
 
@@ -84,6 +85,17 @@ __device__ __forceinline__ void tk_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Barrier `id` over `nthreads` threads (whole warps).
+__device__ __forceinline__ void group_sync_id(int id, int nthreads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
 // kind::f16, f16 x f16 -> f32, M = 128; the B operand K-major or MN-major.
@@ -111,6 +123,14 @@ __device__ __forceinline__ void tk_st32(uint32_t taddr, const uint32_t* v) {
       "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]),
       "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
       "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tk_st16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, "
+      "%13, %14, %15, %16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ void tk_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -184,14 +204,15 @@ __global__ void __launch_bounds__(kTkThreads, 1)
     kv_attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                       const KvAttnArgs a, const TkPlan pl) {
   using L = TkLayout<DP, PERKEY>;
-  constexpr int NS = L::kStages;
+  constexpr int NS = kTkStages;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  // rings of K and V: [2][NS]; buffers and streams: [2]
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::bars);
-  uint64_t *raw_empty = raw_full + 4, *k_full = raw_full + 8, *k_empty = raw_full + 10, *v_full = raw_full + 12,
-           *v_empty = raw_full + 14, *s_full = raw_full + 16, *p_full = raw_full + 18, *o_done = raw_full + 20,
-           *q_full = raw_full + 22, *q_empty = raw_full + 24, *o_free = raw_full + 25;
+  uint64_t *raw_empty = raw_full + 2 * NS, *k_full = raw_empty + 2 * NS, *k_empty = k_full + 1,
+           *v_full = k_empty + 1, *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2,
+           *o_done = p_full + 2, *q_full = o_done + 2, *q_empty = q_full + 2, *o_free = q_empty + 1;
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   volatile int* s_abort = misc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
@@ -239,13 +260,13 @@ __global__ void __launch_bounds__(kTkThreads, 1)
   if (tid == 0) {
     *s_abort = 0;
     *s_turn = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2 * NS; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
     }
+    mbar_init(k_full, 4);
+    mbar_init(k_empty, 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&k_full[i], 4);
-      mbar_init(&k_empty[i], 1);
       mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], 1);
       mbar_init(&s_full[i], 1);
@@ -283,7 +304,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         base += n * items;
       }
   }
-  if (warp == 13) tmem_alloc(tmem_slot, 512);
+  if (warp == 17) tmem_alloc(tmem_slot, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -291,13 +312,14 @@ __global__ void __launch_bounds__(kTkThreads, 1)
   TkWalk walk(a, pl, s_where, u_begin, u_end);
   TkSeg sg;
 
-  if (warp >= 12) {
+  // The launch's 96 registers a thread: 256 x 136 + 256 x 64 + 128 x 72 <= 640 x 96.
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-    if (warp != 13) {
+    if (warp != 17) {
       // ================================================================ producers
       // Three warps take the tiles in turns, so that three chains of look-ups
       // are under way; the copies are issued in the order of the tiles.
-      const uint32_t pw = warp == 12 ? 0 : warp - 13;
+      const uint32_t pw = warp == 16 ? 0 : warp - 17;
       const int copies = kTkKeys / pl.hb;
       const int oob = a.n_blocks * a.H * a.P;  // a row past the cache: reads zeros
       constexpr int NE = PERKEY ? 4 : 1;       // scale entries a lane looks up
@@ -348,11 +370,12 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             break;
           }
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-            const uint32_t r = 2 * n + kv, st = r % NS, ph = (r / NS) & 1;
+          for (int i2 = 0; i2 < 4; ++i2) {  // halves of K, halves of V
+            const int kv = i2 >> 1, half = i2 & 1;
+            const uint32_t r = 2 * n + half, st = kv * NS + r % NS, ph = (r / NS) & 1;
             ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&raw_empty[st], ph ^ 1, s_abort, a.status));
             if (!ok) break;
-            if (kv == 0) {
+            if (i2 == 0) {
 #pragma unroll
               for (int i = 0; i < NE; ++i)
                 if (i * 32 + lane < L::kPer) pages[(size_t)(n % kTkMeta) * L::kPer + i * 32 + lane] = x[i];
@@ -361,10 +384,12 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             if (lane == 0) mbar_arrive_expect_tx(&raw_full[st], L::kRaw);
             __syncwarp();
             unsigned char* dst = smem + L::raw + (size_t)st * L::kRaw;
+            const int first = half * (copies / 2);
 #pragma unroll
             for (int i = 0; i < NE; ++i) {
-              const int c = i * 32 + lane;
-              if (c < copies) tma_load_2d(dst + c * pl.hb * DP, kv ? &map_v : &map_k, 0, row[i], &raw_full[st]);
+              const int c = i * 32 + lane - first;
+              if (c >= 0 && c < copies / 2)
+                tma_load_2d(dst + c * pl.hb * DP, kv ? &map_v : &map_k, 0, row[i], &raw_full[st]);
             }
             __syncwarp();
           }
@@ -373,7 +398,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         }
       }
       if (bits) atomicOr(a.status, bits);
-    } else if (warp == 13) {
+    } else if (warp == 17) {
       // ================================================================ MMA
       const uint32_t q_s = smem_u32(smem + L::q), k_s = smem_u32(smem + L::k16), v_s = smem_u32(smem + L::v16);
       constexpr uint32_t kBlk = kTkKeys * 128;  // bytes of a 64-column block
@@ -381,7 +406,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
       int seg = 0;
       bool ok = true;
       auto await = [&](uint64_t* bar, uint32_t ph) {
-        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(bar, ph, s_abort, a.status));
+        ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_spin(bar, ph, s_abort, a.status));
         return ok;
       };
       auto pv = [&](uint32_t i, bool acc) {
@@ -389,6 +414,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         if (!await(&v_full[b], ph) || !await(&p_full[b], ph)) return;
         tc_fence_after();
         if (lane == 0) {
+#pragma unroll
           for (int k = 0; k < kTkKeys / 16; ++k)
             tk_mma_ts(tmem + 256 + b * 128, tmem + b * 128 + k * 8,
                       tk_desc_mn(v_s + b * L::kOp + k * 2048, kBlk), tk_idesc(DP, true), acc || k > 0);
@@ -402,14 +428,15 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         const uint32_t n0 = n, n1 = n + (sg.t1 - sg.t0);
         for (; n < n1 && ok; ++n) {
           const uint32_t b = n & 1;
-          if (!await(&k_full[b], (n >> 1) & 1)) break;
+          if (!await(k_full, n & 1)) break;
           tc_fence_after();
           if (lane == 0) {
+#pragma unroll
             for (int k = 0; k < DP / 16; ++k)
               umma_bf16(tmem + b * 128, umma_desc_sw128(q_s + (k >> 2) * kBlk + (k & 3) * 32),
-                        umma_desc_sw128(k_s + b * L::kOp + (k >> 2) * kBlk + (k & 3) * 32), tk_idesc(128, false),
+                        umma_desc_sw128(k_s + (k >> 2) * kBlk + (k & 3) * 32), tk_idesc(128, false),
                         k > 0);
-            umma_commit(&k_empty[b]);
+            umma_commit(k_empty);
             umma_commit(&s_full[b]);
             if (n + 1 == n1) umma_commit(q_empty);
           }
@@ -427,8 +454,9 @@ __global__ void __launch_bounds__(kTkThreads, 1)
     }
   } else if (warp >= 8) {
     // ================================================================== converters
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    const int ct = tid - 256;  // 0 .. 127
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    const int ct = tid & 127;       // within the warpgroup
+    const int kv = (warp >> 2) - 2;  // the keys' or the values'
     uint32_t n = 0;
     int seg = 0;
     bool ok = true;
@@ -439,21 +467,25 @@ __global__ void __launch_bounds__(kTkThreads, 1)
     while (ok && walk.next(sg, bits)) {
       // ---- queries: a thread per row, once the last item's scores are done;
       // factors, limits and NaN positions have the places of the item before
-      if (seg > 0 && !await(q_empty, (seg - 1) & 1)) break;
+      if (kv == 0 && seg > 0 && !await(q_empty, (seg - 1) & 1)) break;
       if (seg > 1 && !await(&o_free[seg & 1], ((seg - 2) >> 1) & 1)) break;
       const int sb = (seg & 1) * 128;
-      {
+      if (kv) s_nan[sb + ct] = INT32_MAX;
+      group_sync_id(2 + kv, 128);  // before a value's NaN is noted
+      if (!kv) {
         const int m = ct;
         const bool use = m < sg.nrow;
         const int tt = use ? m / sg.nh : 0;
         const int64_t r = (int64_t)sg.b * a.T + sg.tk + tt;
         const uint16_t* src = a.q + r * a.ldq + (int64_t)(sg.h0 + m - tt * sg.nh) * a.D;
-        uint4 v[DP / 8];
+        auto piece = [&](int i) {
+          return use && i * 8 < a.D ? __ldg(reinterpret_cast<const uint4*>(src + i * 8)) : make_uint4(0u, 0u, 0u, 0u);
+        };
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < DP / 8; ++i) {
-          v[i] = use && i * 8 < a.D ? __ldg(reinterpret_cast<const uint4*>(src + i * 8)) : make_uint4(0u, 0u, 0u, 0u);
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          const uint4 v = piece(i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t lo = w[k] & 0x7FFFu, hi = (w[k] >> 16) & 0x7FFFu;
@@ -465,9 +497,10 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         e = e < 1 ? 1 : (e > 252 ? 252 : e);
         const float f = __int_as_float((254 - e) << 23);
         unsigned char* row = smem + L::q + m * 128;
-#pragma unroll
-        for (int i = 0; i < DP / 8; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll 4
+        for (int i = 0; i < DP / 8; ++i) {  // (again, from the L1)
+          const uint4 v = piece(i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
           uint32_t o[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
@@ -477,44 +510,34 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         }
         s_qf[sb + m] = a.scale * 1.44269504088896340736f * __int_as_float(e << 23);
         s_lim[sb + m] = use ? kv_count(a, r, bits) : 0;
-        s_nan[sb + m] = INT32_MAX;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[seg & 1]);
       }
       for (int t = sg.t0; t < sg.t1 && ok; ++t, ++n) {
-        const uint32_t b = n & 1, ph = (n >> 1) & 1;
-        const int left = sg.max_count - t * kTkKeys;         // keys that some row sees
-        const bool mixed = (t + 1) * kTkKeys > sg.min_count;  // not all rows see all of them
-#pragma unroll
-        for (int kv = 0; kv < 2 && ok; ++kv) {
-          const uint32_t r = 2 * n + kv, st = r % NS;
-          if (!await(&raw_full[st], (r / NS) & 1) || !await(kv ? &v_empty[b] : &k_empty[b], ph ^ 1)) break;
+        const uint32_t b = n & 1;
+        const int left = sg.max_count - t * kTkKeys;  // keys that some row sees
+        // not all rows see all of the keys: values to be zeroed or noted
+        const bool mixed = kv && (t + 1) * kTkKeys > sg.min_count;
+        unsigned char* dst = smem + (kv ? L::v16 + b * L::kOp : L::k16);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const uint32_t r = 2 * n + half, st = kv * NS + r % NS;
+          if (!await(&raw_full[st], (r / NS) & 1)) break;
+          if (half == 0 && !(kv ? await(&v_empty[b], ((n >> 1) & 1) ^ 1) : await(k_empty, (n & 1) ^ 1))) break;
           const unsigned char* src = smem + L::raw + (size_t)st * L::kRaw;
-          unsigned char* dst = smem + (kv ? L::v16 : L::k16) + b * L::kOp;
-          // 16 codes a step: eight rows of one piece column side by side
+          // 16 codes a step, eight rows of a piece column side by side; a warp
+          // takes 16 rows
           constexpr int PC = DP / 16;  // pieces of a row
-#pragma unroll 4
-          for (int i = 0; i < PC; ++i) {
-            // lane: row (3 bits), then the piece; a warp takes 32 rows
-            const int row = (ct >> 5) * 32 + (i * 4 / PC) * 8 + (lane & 7);
-            const int pc = ((i * 4) % PC + (lane >> 3)) % PC;
+          auto place = [&](int i, int& row, int& pc) {
+            row = (warp & 3) * 16 + (i * 4 / PC) * 8 + (lane & 7);
+            pc = ((i * 4) % PC + (lane >> 3)) % PC;
             const int at = DP == 64 ? (pc ^ ((row >> 1) & 3)) : (pc ^ (row & 7));
-            uint4 w = *reinterpret_cast<const uint4*>(src + row * DP + at * 16);
-            if (kv && row >= left) w = make_uint4(0u, 0u, 0u, 0u);
-            if (kv && FMT == kKvE4m3 && mixed) {
-              auto clean = [&](uint32_t c, int k) {
-                uint32_t hit = ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                while (hit) {
-                  const int y = (__ffs(hit) - 1) >> 3;
-                  hit &= hit - 1;
-                  atomicMin(&s_nan[sb + pc * 16 + k * 4 + y], t * kTkKeys + row);
-                  c &= ~(0xFFu << (8 * y));
-                }
-                return c;
-              };
-              w = make_uint4(clean(w.x, 0), clean(w.y, 1), clean(w.z, 2), clean(w.w, 3));
-            }
+            const uint4 w = *reinterpret_cast<const uint4*>(src + row * DP + at * 16);
+            row += half * kTkHalf;
+            return w;
+          };
+          auto store = [&](const uint4& w, int row, int pc) {
             uint32_t o[8];
             codes4<FMT, false>(w.x, o[0], o[1]);
             codes4<FMT, false>(w.y, o[2], o[3]);
@@ -524,12 +547,41 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             const int c2 = (pc & 3) * 2;
             *reinterpret_cast<uint4*>(d + ((c2 ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+          };
+          if (!mixed) {
+#pragma unroll
+            for (int i = 0; i < PC / 2; ++i) {
+              int row, pc;
+              const uint4 w = place(i, row, pc);
+              store(w, row, pc);
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < PC / 2; ++i) {
+              int row, pc;
+              uint4 w = place(i, row, pc);
+              if (row >= left) w = make_uint4(0u, 0u, 0u, 0u);
+              if (FMT == kKvE4m3) {
+                auto clean = [&](uint32_t c, int k) {
+                  uint32_t hit = ((c & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  while (hit) {
+                    const int y = (__ffs(hit) - 1) >> 3;
+                    hit &= hit - 1;
+                    atomicMin(&s_nan[sb + pc * 16 + k * 4 + y], t * kTkKeys + row);
+                    c &= ~(0xFFu << (8 * y));
+                  }
+                  return c;
+                };
+                w = make_uint4(clean(w.x, 0), clean(w.y, 1), clean(w.z, 2), clean(w.w, 3));
+              }
+              store(w, row, pc);
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&raw_empty[st]);
-            mbar_arrive(kv ? &v_full[b] : &k_full[b]);
+            if (half) mbar_arrive(kv ? &v_full[b] : k_full);
           }
         }
       }
@@ -537,11 +589,10 @@ __global__ void __launch_bounds__(kTkThreads, 1)
     }
   } else {
     // ===================================================================== softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 136;");
     const int wg = warp >> 2, row = tid & 127;  // stream; query row
     const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);  // this warp's 32 TMEM lanes
     const uint32_t s_t = lanes + wg * 128;
-    const float sign = a.scale < 0.f ? -1.f : 1.f;
     uint32_t n = 0;
     int seg = 0;
     bool ok = true;
@@ -562,37 +613,37 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         if (!await(&s_full[wg], (n >> 1) & 1)) break;
         tc_fence_after();
         const KvPage* pg = pages + (size_t)(n % kTkMeta) * L::kPer;
-        const bool all = (t + 1) * kTkKeys <= sg.min_count;  // every row sees every key
-        const int seen = lim - t * kTkKeys;                  // keys that this row sees
+        // every row sees every key (a negative softmax scale goes the long way)
+        const bool all = (t + 1) * kTkKeys <= sg.min_count && a.scale >= 0.f;
+        const int seen = lim - t * kTkKeys;  // keys that this row sees
         // the row's maximum; one scale and no mask: of the scores as they are
         float top = -INFINITY;
         auto maxima = [&](auto all_tag) {
           constexpr bool ALL = decltype(all_tag)::value;
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            uint32_t x[2][32];
-            tmem_ld32_nowait(s_t + c * 32, x[0]);
-            tmem_ld32_nowait(s_t + c * 32 + 32, x[1]);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            tmem_ld32_nowait(s_t + c * 32, x);
+            const KvPage e = pg[PERKEY ? 0 : c];
             tmem_ld_wait();
-#pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const KvPage e = pg[PERKEY ? 0 : c + y];
-              float m0 = -INFINITY, m1 = -INFINITY;
+            float m0 = -INFINITY, m1 = -INFINITY;
+            if (PERKEY || !ALL) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) {
-                float v = __uint_as_float(x[y][j]);
-                if (PERKEY || !ALL) {
-                  const KvPage k = PERKEY ? pg[PERKEY ? (c + y) * 32 + j : 0] : e;
-                  v = fmaf(v, k.ks * qf, k.lv);
-                  if (!ALL && (c + y) * 32 + j >= seen) v = -INFINITY;
-                } else {
-                  v *= sign;
-                }
+                const KvPage k = PERKEY ? pg[PERKEY ? c * 32 + j : 0] : e;
+                float v = fmaf(__uint_as_float(x[j]), k.ks * qf, k.lv);
+                if (!ALL && c * 32 + j >= seen) v = -INFINITY;
                 if (j & 1) m1 = fmaxf(m1, v);
                 else m0 = fmaxf(m0, v);
               }
-              m0 = fmaxf(m0, m1);
-              top = fmaxf(top, PERKEY || !ALL ? m0 : fmaf(m0 * sign, e.ks * qf, e.lv));
+              top = max3(top, m0, m1);
+            } else {  // the factor is not negative: the maximum of the scores as they are
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                m0 = max3(m0, __uint_as_float(x[j]), __uint_as_float(x[j + 1]));
+                m1 = max3(m1, __uint_as_float(x[j + 2]), __uint_as_float(x[j + 3]));
+              }
+              top = fmaxf(top, fmaf(fmaxf(m0, m1), e.ks * qf, e.lv));
             }
           }
         };
@@ -622,44 +673,40 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         // the weights, 16 columns for 32 scores, behind the scores still to read
         auto weights = [&](auto all_tag) {
           constexpr bool ALL = decltype(all_tag)::value;
-#pragma unroll
-          for (int c = 0; c < 4; c += 2) {
-            uint32_t x[2][32], w[32];
-            tmem_ld32_nowait(s_t + c * 32, x[0]);
-            tmem_ld32_nowait(s_t + c * 32 + 32, x[1]);
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], w[16];
+            tmem_ld32_nowait(s_t + c * 32, x);
+            const KvPage e = pg[PERKEY ? 0 : c];
+            const float f = e.ks * qf, d = e.lv - z;
             tmem_ld_wait();
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              const KvPage e = pg[PERKEY ? 0 : c + y];
-              const float f = e.ks * qf, d = e.lv - z;
-              float s0 = 0.f, s1 = 0.f;
+            for (int j = 0; j < 32; j += 2) {
+              float p[2];
 #pragma unroll
-              for (int j = 0; j < 32; j += 2) {
-                float p[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const float v = __uint_as_float(x[y][j + k]);
-                  if (PERKEY) {
-                    const KvPage g = pg[PERKEY ? (c + y) * 32 + j + k : 0];
-                    p[k] = ex2(fmaf(v, g.ks * qf, g.lv - z));
-                    if (!ALL && (c + y) * 32 + j + k >= seen) p[k] = 0.f;
-                    l = fmaf(p[k], g.iv, l);
-                    p[k] *= g.rest;
-                  } else {
-                    p[k] = ex2(fmaf(v, f, d));
-                    if (!ALL && (c + y) * 32 + j + k >= seen) p[k] = 0.f;
-                    (k ? s1 : s0) += p[k];
-                  }
+              for (int k = 0; k < 2; ++k) {
+                const float v = __uint_as_float(x[j + k]);
+                if (PERKEY) {
+                  const KvPage g = pg[PERKEY ? c * 32 + j + k : 0];
+                  p[k] = ex2(fmaf(v, g.ks * qf, g.lv - z));
+                  if (!ALL && c * 32 + j + k >= seen) p[k] = 0.f;
+                  l = fmaf(p[k], g.iv, l);
+                  p[k] *= g.rest;
+                } else {
+                  p[k] = ex2(fmaf(v, f, d));
+                  if (!ALL && c * 32 + j + k >= seen) p[k] = 0.f;
+                  (k ? s1 : s0) += p[k];
                 }
-                if (!PERKEY && e.rest != 1.f) {
-                  p[0] *= e.rest;
-                  p[1] *= e.rest;
-                }
-                w[y * 16 + (j >> 1)] = pack_f16(p[0], p[1]);
               }
-              if (!PERKEY) l = fmaf(s0 + s1, e.iv, l);
+              if (!PERKEY && e.rest != 1.f) {
+                p[0] *= e.rest;
+                p[1] *= e.rest;
+              }
+              w[j >> 1] = pack_f16(p[0], p[1]);
             }
-            tk_st32(s_t + c * 16, w);
+            if (!PERKEY) l = fmaf(s0 + s1, e.iv, l);
+            tk_st16(s_t + c * 16, w);
           }
         };
         if (all) weights(std::true_type());
@@ -812,7 +859,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
     }
   }
   __syncthreads();
-  if (warp == 13) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 template <int FMT, int DP, bool PERKEY>
@@ -845,7 +892,7 @@ cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, int num_sms, cudaStream_t str
   pl.TT = fit < a.T ? fit : a.T;
   pl.ntb = (a.T + pl.TT - 1) / pl.TT;
   const int low = a.P & -a.P;  // the largest power of two in P
-  pl.hb = low < kTkKeys ? low : kTkKeys;
+  pl.hb = low < kTkHalf ? low : kTkHalf;
   pl.ws = a.ws;
   pl.arrive = a.arrive;
   CUtensorMap mk, mv;
