@@ -93,11 +93,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Barrier `id` over `nthreads` threads (whole warps).
-__device__ __forceinline__ void group_sync_id(int id, int nthreads) {
-  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
-}
-
 // kind::f16, f16 x f16 -> f32, M = 128; the B operand K-major or MN-major.
 constexpr uint32_t tk_idesc(int N, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -257,6 +252,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
     if (lane >= o) incl += n;
   }
   if (lane == 31) s_warp[warp] = incl;
+  if (tid < 256) s_nan[tid] = INT32_MAX;
   if (tid == 0) {
     *s_abort = 0;
     *s_turn = 0;
@@ -470,8 +466,6 @@ __global__ void __launch_bounds__(kTkThreads, 1)
       if (kv == 0 && seg > 0 && !await(q_empty, (seg - 1) & 1)) break;
       if (seg > 1 && !await(&o_free[seg & 1], ((seg - 2) >> 1) & 1)) break;
       const int sb = (seg & 1) * 128;
-      if (kv) s_nan[sb + ct] = INT32_MAX;
-      group_sync_id(2 + kv, 128);  // before a value's NaN is noted
       if (!kv) {
         const int m = ct;
         const bool use = m < sg.nrow;
@@ -794,6 +788,8 @@ __global__ void __launch_bounds__(kTkThreads, 1)
       tc_fence_before();
       if (part) __threadfence();
       group_sync(kTkSoft);  // limits, NaN positions and accumulators have been read
+      if (wg == 0) s_nan[sb + row] = INT32_MAX;  // for the item after the next
+      __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[seg & 1]);
       if (part && !aborted) {
         const int64_t c0 = ((sg.unit0 + 1) * nc + W - 1) / W - 1;
