@@ -63,7 +63,7 @@ namespace idx {
 constexpr int kKvProducers = 4;
 constexpr int kKvUnit = 32;        // keys per unit
 constexpr int kKvMaxStages = 32;
-constexpr int kKvBatch = 4;        // units the producer issues at once
+constexpr int kKvMaxBatch = 8;     // units the producer issues at once, at most
 constexpr int kKvCharge = 8;       // units that an item's start and end count for in the split
 constexpr int kKvSegs = 64;        // descriptor ring: more than the stages and a group of warps
 constexpr int kKvSmem = 227 * 1024;
@@ -135,6 +135,12 @@ struct KvLayout {
   static constexpr int stages() {
     const int n = (int)((kKvSmem - 1024 - ring) / kStage);
     return n < kKvMaxStages ? n : kKvMaxStages;
+  }
+  // A batch waits for all of its stages.  At an item's end every group but the
+  // last may hold a stage of the next item (that is how it learns of the end)
+  // until the last one has met them: what is left must hold a batch.
+  static constexpr int batch() {
+    return stages() - KG + 1 < kKvMaxBatch ? stages() - KG + 1 : kKvMaxBatch;
   }
   static constexpr size_t total() { return ring + (size_t)stages() * kStage + 1024; }
   static_assert(NC % RG == 0 && stages() >= KG, "each group of warps needs a stage");
@@ -472,11 +478,12 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
               valid = false;
             }
           }
-          KvPage pg{0.f, 0.f, 0.f, 0.f};
+          float ks = 0.f, vs = 0.f;
           int pos = INT32_MAX, row = 0, nk = 0;
           if (valid) {
             const int64_t cell = (int64_t)id * a.H + g;
-            pg = kv_scales(__ldg(a.k_scale + cell), __ldg(a.v_scale + cell));
+            ks = __ldg(a.k_scale + cell);  // (not waited for before the copies are issued)
+            vs = __ldg(a.v_scale + cell);
             pos = p * a.P + sub;
             row = (int)(cell * a.P) + sub;
             nk = a.P - sub < kKvUnit ? a.P - sub : kKvUnit;
@@ -519,15 +526,27 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
             my -= ns;
             my_phase ^= 1;
           }
-          // kKvBatch units at a time, every lane for itself: a stage is filled
+          // batch() units at a time, every lane for itself: a stage is filled
           // as soon as the batch's last one is free
-          for (int b0 = 0; b0 < found && ok; b0 += kKvBatch) {
-            const bool go = busy && place >= b0 && place < b0 + kKvBatch;
+          for (int b0 = 0; b0 < found && ok; b0 += L::batch()) {
+            const bool go = busy && place >= b0 && place < b0 + L::batch();
             bool got = true;
             if (go) got = mbar_wait_bounded(&empty[my], my_phase, s_abort, a.status);
             ok = __all_sync(0xFFFFFFFFu, got);
             if (!ok) break;
+            // The copies first: their bytes may arrive before they are expected,
+            // the phase still waits for the arrival that expects them.
+            if (go && valid) {
+              unsigned char* dst = ring + (size_t)my * L::kStage +
+                                   (MULTI ? (lane - unit * pl.ppt) * pl.pitch : 0) * L::RB;
+#pragma unroll
+              for (int cb = 0; cb < L::NB; ++cb) {
+                tma_load_2d(dst + cb * kKvUnit * L::RB, &map_k, cb * L::RB, row, &full[my]);
+                tma_load_2d(dst + (L::NB + cb) * kKvUnit * L::RB, &map_v, cb * L::RB, row, &full[my]);
+              }
+            }
             if (go) {
+              const KvPage pg = valid ? kv_scales(ks, vs) : KvPage{0.f, 0.f, 0.f, 0.f};
               if (MULTI) {  // entries of the page's keys
                 const int k = lane - unit * pl.ppt;
                 for (int i = 0; i < a.P; ++i) {
@@ -549,16 +568,6 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
             if (go && leads)
               mbar_arrive_expect_tx(&full[my], (uint32_t)__popc(vmask & who) * 2u * L::NB * L::RB *
                                                    (uint32_t)pl.box);
-            if (MULTI) __syncwarp();
-            if (go && valid) {
-              unsigned char* dst = ring + (size_t)my * L::kStage +
-                                   (MULTI ? (lane - unit * pl.ppt) * pl.pitch : 0) * L::RB;
-#pragma unroll
-              for (int cb = 0; cb < L::NB; ++cb) {
-                tma_load_2d(dst + cb * kKvUnit * L::RB, &map_k, cb * L::RB, row, &full[my]);
-                tma_load_2d(dst + (L::NB + cb) * kKvUnit * L::RB, &map_v, cb * L::RB, row, &full[my]);
-              }
-            }
             __syncwarp();
           }
           if (ok && busy && valid) {

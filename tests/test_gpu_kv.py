@@ -333,6 +333,15 @@ def test_attention_causal_tokens(ctx, T, Q, H):
     check_attn(ctx, attn_case(T + Q, 3, T, Q, H, 128, 16, N, "e4m3", counts))
 
 
+@pytest.mark.parametrize("Q,P", [(16, 16), (12, 4), (4, 16), (16, 64), (40, 8)])
+def test_attention_many_short_items_wide_heads(ctx, Q, P):
+    # the ring of stages at its smallest beside the groups of warps, and items
+    # that end within it: groups wait for one another while they hold stages
+    rng = np.random.default_rng(Q + P)
+    counts = rng.integers(1, 700, (90, 1))
+    check_attn(ctx, attn_case(Q + P, 90, 1, Q * 2, 2, 256, P, -(-700 // P), "int8", counts))
+
+
 @pytest.mark.parametrize("B,T,Q,H,D,P,pos0,fmt", [
     (1, 17, 4, 1, 64, 32, 0, "int8"), (1, 33, 4, 1, 128, 64, 0, "e4m3"), (2, 40, 8, 2, 128, 64, 900, "e4m3"),
     (2, 40, 8, 2, 128, 64, 900, "int8"), (1, 130, 4, 1, 64, 128, 257, "e4m3"), (1, 9, 16, 2, 128, 256, 1000, "int8"),
