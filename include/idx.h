@@ -217,7 +217,8 @@ IDX_API int kmeans_scores(idx_ctx* ctx, const uint16_t* x, const uint16_t* centr
  *   slot              block * P + row of a token, -1 for none
  *
  * D a multiple of 16 and at most 256; n_blocks * H * P and N * P below 2^31.
- * The limits given to idx_init do not bind these calls.  Their batches are
+ * The limits given to idx_init do not bind these calls (kv_attention uses a part
+ * of the workspace whose size is fixed; the others use none).  Their batches are
  * [B][T] rows, T tokens per request; a request with fewer is padded (slot -1,
  * key count 0).
  */
