@@ -64,9 +64,16 @@
 #include "kv.cuh"
 #include "tc.cuh"
 
+// A test build defines this as a condition under which a CTA runs as if one of
+// its waits had expired.
+#ifndef IDX_KV_GIVE_UP
+#define IDX_KV_GIVE_UP 0
+#endif
+
 namespace idx {
 
 constexpr int kKvProducers = 4;
+constexpr int kKvProducerBarrier = 2;  // the named barrier of the producer warps
 constexpr int kKvUnit = 32;        // keys per unit
 constexpr int kKvMaxStages = 32;
 constexpr int kKvMaxBatch = 8;     // units the producer issues at once, at most
@@ -104,7 +111,8 @@ struct KvSeg {
 // Scales of a stage's keys (one entry, or one per key where a unit has several
 // pages): the score's, log2 and inverse of the value's, and what is left of a
 // value scale below 2^-100.  Beside them the position of the (first) key, and
-// per stage its segment, kKvFull and the number of its keys.
+// per stage its segment, kKvFull, the number of its keys and the parity of its
+// latest pass (-1: never filled).
 struct KvPage {
   float ks, lv, iv, rest;
 };
@@ -335,8 +343,9 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
     mbar_init(&full[tid], 1);
     mbar_init(&empty[tid], RG);
     fence_mbar_init();
+    meta[tid * 4 + 3] = -1;
   }
-  if (tid == 0) *s_abort = 0;
+  if (tid == 0) *s_abort = IDX_KV_GIVE_UP;
   if (tid < kKvProducers) s_tot[tid] = tid ? ~0ull : 0ull;
   if (MULTI)  // rows between and behind a unit's pages hold no key
     for (int i = tid; i < kKvMaxStages * L::kPages; i += L::kThreads) {
@@ -391,8 +400,6 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
     uint32_t look = 0;            // look-ups so far, of all producers
     int sidx = 0;
     bool ok = true;
-    uint64_t *last0 = nullptr, *last1 = nullptr;  // this lane's latest copies
-    int par0 = 0, par1 = 0;
     // The stages used before look-up `look`, once its predecessor has filled its own.
     auto stages_before = [&](uint32_t& n) {
       for (uint32_t it = 0; it < kMaxWaitIters; ++it) {
@@ -570,6 +577,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
                 meta[my * 4] = sidx;
                 meta[my * 4 + 1] = f ? kKvFull : 0;
                 meta[my * 4 + 2] = nk;
+                meta[my * 4 + 3] = my_phase ^ 1;
               }
             }
             if (MULTI) __syncwarp();
@@ -577,12 +585,6 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
               mbar_arrive_expect_tx(&full[my], (uint32_t)__popc(vmask & who) * 2u * L::NB * L::RB *
                                                    (uint32_t)pl.box);
             __syncwarp();
-          }
-          if (ok && busy && valid) {
-            last1 = last0;
-            par1 = par0;
-            last0 = &full[my];
-            par0 = my_phase ^ 1;
           }
           if (ok && none) {
             ok = __all_sync(0xFFFFFFFFu,
@@ -596,6 +598,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
               meta[slot * 4] = sidx;
               meta[slot * 4 + 1] = 0;
               meta[slot * 4 + 2] = 0;
+              meta[slot * 4 + 3] = phase ^ 1;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[slot]);
@@ -622,17 +625,16 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
         ok = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&empty[slot], phase, s_abort, a.status));
         if (ok && lane == 0) {
           meta[slot * 4] = INT32_MAX;
+          meta[slot * 4 + 3] = phase ^ 1;
           mbar_arrive(&full[slot]);
         }
         __syncwarp();
       }
     }
-    // The consumers wait for every stage; where they gave up, this lane's
-    // copies in flight end first (a stage used again since counts as ended).
-    if (!ok) {
-      for (int i = 0; last1 && i < (1 << 20) && !mbar_test_wait(last1, par1); ++i) {}
-      for (int i = 0; last0 && i < (1 << 20) && !mbar_test_wait(last0, par0); ++i) {}
-    }
+    // The copies end before the CTA does, whether or not they are still waited
+    // for: of each stage the latest, its earlier ones ended before it.
+    asm volatile("bar.sync %0, %1;" ::"n"(kKvProducerBarrier), "n"(kKvProducers * 32) : "memory");
+    if (pw == 0 && lane < ns && meta[lane * 4 + 3] >= 0) mbar_wait_drain(&full[lane], (uint32_t)meta[lane * 4 + 3]);
     if (bits) atomicOr(a.status, bits);
     return;
   }
@@ -1176,7 +1178,6 @@ template <int DP>
 cudaError_t launch_kv_attn_dp(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& a,
                               KvPlan pl, int nt, int rg, int grid, cudaStream_t stream);
 
-#ifdef IDX_KV_ATTN_DP
 template <int FMT, int DP, int NT, int RG, bool MULTI>
 static cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& a,
                               KvPlan& pl, int grid, cudaStream_t stream) {
@@ -1190,6 +1191,7 @@ static cudaError_t launch_one(const CUtensorMap& mk, const CUtensorMap& mv, cons
   return cudaGetLastError();
 }
 
+#ifdef IDX_KV_ATTN_DP
 template <>
 cudaError_t launch_kv_attn_dp<IDX_KV_ATTN_DP>(const CUtensorMap& mk, const CUtensorMap& mv,
                                               const KvAttnArgs& a, KvPlan pl, int nt, int rg,

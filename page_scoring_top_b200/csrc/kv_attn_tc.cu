@@ -62,7 +62,7 @@ struct TkLayout {
   static constexpr int kOp = kTkKeys * DP * 2;        // bytes of a 128-row operand
   static constexpr int kRaw = kTkHalf * DP;           // bytes of half a tile's codes
   static constexpr int kPer = PERKEY ? kTkKeys : 4;   // scale entries of a tile
-  static constexpr size_t bars = 0;                   // 36 barriers
+  static constexpr size_t bars = 0;                   // 38 barriers
   static constexpr size_t misc = 384;                 // 64 ints
   static constexpr size_t rows = misc + 256;          // factor, limit (two items'); m, l of two streams
   static constexpr size_t nanpos = rows + 2 * 128 * 8 + 512 * 4;  // first position of a NaN per column
@@ -211,13 +211,15 @@ __global__ void __launch_bounds__(kTkThreads, 1)
   uint64_t* raw_full = reinterpret_cast<uint64_t*>(smem + L::bars);
   uint64_t *raw_empty = raw_full + 2 * NS, *k_full = raw_empty + 2 * NS, *k_empty = k_full + 1,
            *v_full = k_empty + 1, *v_empty = v_full + 2, *s_full = v_empty + 2, *p_full = s_full + 2,
-           *o_done = p_full + 2, *q_full = o_done + 2, *q_empty = q_full + 2, *o_free = q_empty + 1;
+           *o_done = p_full + 2, *q_full = o_done + 2, *q_empty = q_full + 2, *o_free = q_empty + 1,
+           *m_done = o_free + 2;
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   volatile int* s_abort = misc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
   int* s_flag = misc + 2;
   volatile uint32_t* s_turn = reinterpret_cast<volatile uint32_t*>(misc + 4);  // next tile to be fetched
-  int64_t* s_where = reinterpret_cast<int64_t*>(misc + 8);
+  int64_t* s_where = reinterpret_cast<int64_t*>(misc + 8);  // row tile, units before it
+  int* s_part = misc + 12;  // copied stages of the first tile that was not fetched whole
   long long* s_warp = reinterpret_cast<long long*>(misc + 24);
   float* s_qf = reinterpret_cast<float*>(smem + L::rows);
   int* s_lim = reinterpret_cast<int*>(s_qf + 256);
@@ -258,8 +260,9 @@ __global__ void __launch_bounds__(kTkThreads, 1)
   if (lane == 31) s_warp[warp] = incl;
   if (tid < 256) s_nan[tid] = INT32_MAX;
   if (tid == 0) {
-    *s_abort = 0;
+    *s_abort = IDX_KV_GIVE_UP;
     *s_turn = 0;
+    *s_part = 0;
     for (int i = 0; i < 2 * NS; ++i) {
       mbar_init(&raw_full[i], 1);
       mbar_init(&raw_empty[i], 4);
@@ -278,6 +281,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
       mbar_init(&o_free[i], 8);
     }
     mbar_init(q_empty, 1);
+    mbar_init(m_done, 1);
     fence_mbar_init();
   }
   __syncthreads();
@@ -374,7 +378,10 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             const int kv = i2 >> 1, half = i2 & 1;
             const uint32_t r = 2 * n + half, st = kv * NS + r % NS, ph = (r / NS) & 1;
             ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&raw_empty[st], ph ^ 1, s_abort, a.status));
-            if (!ok) break;
+            if (!ok) {
+              if (lane == 0) *s_part = i2;
+              break;
+            }
             if (i2 == 0) {
 #pragma unroll
               for (int i = 0; i < NE; ++i)
@@ -396,6 +403,14 @@ __global__ void __launch_bounds__(kTkThreads, 1)
           __threadfence_block();
           if (ok && lane == 0) *s_turn = n + 1;
         }
+      }
+      // The copies end before the CTA does, whether or not they are still
+      // waited for: of each stage the latest, its earlier ones ended before it.
+      asm volatile("bar.sync %0, 96;" ::"n"(kKvProducerBarrier) : "memory");
+      if (pw == 0 && lane < 2 * NS) {
+        const int kv = lane / NS, st = lane - kv * NS, part = *s_part;
+        const int used = 2 * (int)*s_turn + (kv ? (part > 2 ? part - 2 : 0) : (part < 2 ? part : 2));
+        if (used > st) mbar_wait_drain(&raw_full[lane], (uint32_t)((used - 1 - st) / NS) & 1);
       }
       if (bits) atomicOr(a.status, bits);
     } else if (warp == 17) {
@@ -451,6 +466,11 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         pv(n1 - 1, n1 - 1 >= n0 + 2);
         ++seg;
       }
+      // the products end before the TMEM that they write is freed, whether or
+      // not their readers still wait for them
+      if (lane == 0) umma_commit(m_done);
+      __syncwarp();
+      mbar_wait_drain(m_done, 0);
     }
   } else if (warp >= 8) {
     // ================================================================== converters
