@@ -287,6 +287,22 @@ __device__ __forceinline__ KvTile kv_tile(const KvAttnArgs& a, const KvPlan& pl,
   return k;
 }
 
+// An item of nt units from unit0 on, cut over CTAs of which nc share W units:
+// the first of them and how many they are.
+__device__ __forceinline__ int kv_parts(int64_t unit0, int nt, int64_t W, int64_t nc, int64_t& c0) {
+  c0 = ((unit0 + 1) * nc + W - 1) / W - 1;
+  return (int)(((unit0 + nt) * nc + W - 1) / W - 1 - c0) + 1;
+}
+
+// One thread of a CTA is through with its part of such an item, written or not
+// (every CTA arrives, so that the counter is zero again when the call ends).
+// True for the last to arrive.
+__device__ __forceinline__ bool kv_arrive(int32_t* arrive, int64_t c0, int np) {
+  const bool last = atomicAdd(arrive + c0, 1) == np - 1;
+  if (last) arrive[c0] = 0;
+  return last;
+}
+
 template <int FMT, int DP, int NT, int RG, bool MULTI>
 __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
     kv_attn_kernel(const __grid_constant__ CUtensorMap map_k,
@@ -302,6 +318,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
   int* misc = reinterpret_cast<int*>(smem + L::misc);
   volatile int* s_abort = misc;        // misc[0]
   int* s_flag = misc + 2;              // per segment: aborted, last to arrive
+  int* s_done = misc + 4;              // segments ended before the CTA gave up
   int64_t* s_where = reinterpret_cast<int64_t*>(misc + 8);  // row tile, units before, both ends
   long long* s_warp = reinterpret_cast<long long*>(misc + 24);  // warp sums
   volatile unsigned long long* s_tot =  // per look-up: its number, stages before it
@@ -345,7 +362,10 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
     fence_mbar_init();
     meta[tid * 4 + 3] = -1;
   }
-  if (tid == 0) *s_abort = IDX_KV_GIVE_UP;
+  if (tid == 0) {
+    *s_abort = IDX_KV_GIVE_UP;
+    *s_done = 0;
+  }
   if (tid < kKvProducers) s_tot[tid] = tid ? ~0ull : 0ull;
   if (MULTI)  // rows between and behind a unit's pages hold no key
     for (int i = tid; i < kKvMaxStages * L::kPages; i += L::kThreads) {
@@ -988,6 +1008,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
     if (tid == 0) s_flag[0] = *s_abort;
     group_sync(NC * 32);
     const bool aborted = s_flag[0] != 0;
+    if (tid == 0 && !aborted) *s_done = s + 1;
     const bool part = !(sg.first && sg.last);  // the item is in several CTAs
     float* wslot = pl.ws + (int64_t)(2 * blockIdx.x + (sg.first ? 1 : 0)) * kKvSlot;
     const int nh = G - sg.h0 % G < pl.GG ? G - sg.h0 % G : pl.GG;
@@ -1087,17 +1108,11 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
     if (ok && s + 1 < nseg) load_q(segs[(s + 1) % kKvSegs]);
     if (part && !aborted) {
       // the item's CTAs: c0 holds its first unit, c1 its last
-      const int64_t W = s_where[2], nc = s_where[3];
-      const int64_t c0 = ((sg.unit0 + 1) * nc + W - 1) / W - 1;
-      const int64_t c1 = ((sg.unit0 + sg.nt) * nc + W - 1) / W - 1;
-      const int np = (int)(c1 - c0) + 1;
+      int64_t c0;
+      const int np = kv_parts(sg.unit0, sg.nt, s_where[2], s_where[3], c0);
       __threadfence();
       group_sync(NC * 32);
-      if (tid == 0) {
-        const int before_ = atomicAdd(pl.arrive + c0, 1);
-        s_flag[1] = before_ == np - 1;
-        if (before_ == np - 1) pl.arrive[c0] = 0;
-      }
+      if (tid == 0) s_flag[1] = kv_arrive(pl.arrive, c0, np);
       group_sync(NC * 32);
       if (s_flag[1]) {
         __threadfence();
@@ -1161,6 +1176,26 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
         }
         group_sync(NC * 32);  // s_join is free again
       }
+    }
+  }
+  // A CTA that gave up arrives at the items that it did not come to.  Their
+  // descriptors may be missing: the walk of the producers again.
+  if (tid == 0 && *s_done < nseg) {
+    const int64_t W = s_where[2], nc = s_where[3], u1 = W * (blockIdx.x + 1) / nc;
+    int64_t rt = s_where[0], base = s_where[1], u = W * blockIdx.x / nc;
+    for (int s = 0; u < u1; ++rt) {
+      const int nt = kv_tile(a, pl, rt, bits).nt;
+      const int64_t n = nt + kKvCharge, rt_end = base + n * items;
+      while (u < u1 && u < rt_end) {
+        const int64_t it = (u - base) / n, x0 = (u - base) - it * n;
+        const int64_t x1 = n - x0 < u1 - u ? n : x0 + (u1 - u);
+        u += x1 - x0;
+        if (x1 <= kKvCharge) continue;  // charged units only: not this CTA's
+        int64_t c0;
+        const int np = kv_parts(base + it * n + kKvCharge, nt, W, nc, c0);
+        if (s++ >= *s_done && np > 1) kv_arrive(pl.arrive, c0, np);
+      }
+      base = rt_end;
     }
   }
 }

@@ -815,15 +815,10 @@ __global__ void __launch_bounds__(kTkThreads, 1)
       if (wg == 0) s_nan[sb + row] = INT32_MAX;  // for the item after the next
       __syncwarp();
       if (lane == 0) mbar_arrive(&o_free[seg & 1]);
-      if (part && !aborted) {
-        const int64_t c0 = ((sg.unit0 + 1) * nc + W - 1) / W - 1;
-        const int64_t c1 = ((sg.unit0 + sg.nt) * nc + W - 1) / W - 1;
-        const int np = (int)(c1 - c0) + 1;
-        if (tid == 0) {
-          const int before_ = atomicAdd(pl.arrive + c0, 1);
-          s_flag[1] = before_ == np - 1;
-          if (before_ == np - 1) pl.arrive[c0] = 0;
-        }
+      if (part) {
+        int64_t c0;
+        const int np = kv_parts(sg.unit0, sg.nt, W, nc, c0);
+        if (tid == 0) s_flag[1] = kv_arrive(pl.arrive, c0, np) && !aborted;
         group_sync(kTkSoft);
         if (s_flag[1]) {
           __threadfence();

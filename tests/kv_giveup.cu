@@ -6,7 +6,12 @@
 #include <cuda_runtime.h>
 
 __device__ int g_give_up = -1;
-#define IDX_KV_GIVE_UP ((int)blockIdx.x == g_give_up)
+__device__ __forceinline__ bool give_up(int* status) {
+  if ((int)blockIdx.x != g_give_up) return false;
+  atomicOr(status, 2);  // what an expired wait raises
+  return true;
+}
+#define IDX_KV_GIVE_UP give_up(a.status)
 
 #include "kv_attn.cuh"
 
