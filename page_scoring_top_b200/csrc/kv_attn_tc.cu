@@ -56,6 +56,7 @@ constexpr int kTkStages = 5;       // stages of the rings of K and of V
 constexpr int kTkCharge = 4;       // tiles that an item's start and end count for
 constexpr int kTkMeta = 6;         // tiles whose scales are held: up to five are in the pipeline
 constexpr float kTkSlack = 8.f;    // log2 by which a row may exceed its reference
+constexpr float kTkLarge = 8388608.f;  // exponents from here on take the long way
 
 template <int DP, bool PERKEY>
 struct TkLayout {
@@ -688,7 +689,9 @@ __global__ void __launch_bounds__(kTkThreads, 1)
           }
         }
         const float z = m == -INFINITY ? 0.f : m;
-        // the weights, 16 columns for 32 scores, behind the scores still to read
+        // the weights, 16 columns for 32 scores, behind the scores still to read.
+        // One addition for x - z leaves the rounding of x in the exponent; where
+        // that may be large (2^23: half a step is 1/2), x is rounded as z was.
         auto weights = [&](auto all_tag) {
           constexpr bool ALL = decltype(all_tag)::value;
 #pragma unroll 1
@@ -707,12 +710,12 @@ __global__ void __launch_bounds__(kTkThreads, 1)
                 const float v = __uint_as_float(x[j + k]);
                 if (PERKEY) {
                   const KvPage g = pg[PERKEY ? c * 32 + j + k : 0];
-                  p[k] = ex2(fmaf(v, g.ks * qf, g.lv - z));
+                  p[k] = ALL ? ex2(fmaf(v, g.ks * qf, g.lv - z)) : ex2(fmaf(v, g.ks * qf, g.lv) - z);
                   if (!ALL && c * 32 + j + k >= seen) p[k] = 0.f;
                   l = fmaf(p[k], g.iv, l);
                   p[k] *= g.rest;
                 } else {
-                  p[k] = ex2(fmaf(v, f, d));
+                  p[k] = ALL ? ex2(fmaf(v, f, d)) : ex2(fmaf(v, f, e.lv) - z);
                   if (!ALL && c * 32 + j + k >= seen) p[k] = 0.f;
                   (k ? s1 : s0) += p[k];
                 }
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             tk_st16(s_t + c * 16, w);
           }
         };
-        if (all) weights(std::true_type());
+        if (all && !__any_sync(0xFFFFFFFFu, fabsf(z) >= kTkLarge)) weights(std::true_type());
         else weights(std::false_type());
         tk_st_wait();
         tc_fence_before();
