@@ -7,15 +7,18 @@
 // the running maximum and sum of the softmax.
 //
 // The value scale goes into the exponent: with x_i = s_i log2(e) + log2(vs_i)
-// and m the running maximum of x,
-//     p_i = 2^(x_i - m) <= 1,  O += p_i v8_i,  l += p_i / vs_i,
+// and m the running maximum of x less 14,
+//     p_i = 2^(x_i - m) <= 2^14,  O += p_i v8_i,  l += p_i / vs_i,
 //     out = O / l,  lse = (m + log2 l) ln 2.
-// So the weights that meet the codes in the tensor cores are at most 1 and their
-// largest is 1 whatever the scales are, and fp16 holds them to 2^-11: e4m3 and
-// int8 codes are exact in fp16, products are exact and sums are fp32.  fp16
-// holds bf16 queries exactly too, after a power of two per row (its inverse
-// goes into the score's factor).  A value scale below 2^-100 counts as 2^-100 in the
-// exponent, and its weights are multiplied by what is left.
+// So the weights that meet the codes in the tensor cores end at the top of
+// fp16's range whatever the scales are: those down to 2^-28 of the largest are
+// held to 2^-11 of their own size, smaller ones to 2^-39 of the largest (a key
+// with most of the weight and no value, over a long context, leaves the output
+// to them).  e4m3 and int8 codes are exact in fp16, products are exact and sums
+// are fp32.  fp16 holds bf16 queries exactly too, after a power of two per row
+// (its inverse goes into the score's factor).  A value scale below 2^-86 counts
+// as 2^-86 in the exponent (the sum l stays finite), and its weights are
+// multiplied by what is left.
 //
 // Work: a row tile is TT tokens of one request (1 with page lists, which differ
 // by token) and up to 16*MT query rows (tokens x heads of one kv head), an item
@@ -82,7 +85,8 @@ constexpr int kKvMaxBatch = 8;     // units the producer issues at once, at most
 constexpr int kKvCharge = 28;
 constexpr int kKvSegs = 64;        // descriptor ring: more than the stages and a group of warps
 constexpr int kKvSmem = 227 * 1024;
-constexpr float kKvMinScale = 7.8886090522101181e-31f;  // 2^-100
+constexpr float kKvMinScale = 1.2924697071141057e-26f;  // 2^-86
+constexpr float kKvLift = 14.f;  // log2 of the largest weight
 
 // What the host settles for a launch.
 struct KvPlan {
@@ -110,7 +114,7 @@ struct KvSeg {
 
 // Scales of a stage's keys (one entry, or one per key where a unit has several
 // pages): the score's, log2 and inverse of the value's, and what is left of a
-// value scale below 2^-100.  Beside them the position of the (first) key, and
+// value scale below 2^-86.  Beside them the position of the (first) key, and
 // per stage its segment, kKvFull, the number of its keys and the parity of its
 // latest pass (-1: never filled).
 struct KvPage {
@@ -193,6 +197,14 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The weights' pair.  Saturated: where a step of the scores is 8 or more, the
+// reference may round down by it, and a weight reach 2^16.
+__device__ __forceinline__ uint32_t pack_weights(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -859,7 +871,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
                           fmaxf(sc[0][1][n][e], sc[0][1][n][2 + e]));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 4));
           v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16));
+          v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, 16)) - kKvLift;
           top[n][e] = v;
           up |= v > m[n][e];
         }
@@ -899,7 +911,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
               p0 *= g.rest;
               p1 *= g.rest;
             }
-            pb[t][n][e] = transpose8(pack_f16(p0, p1));
+            pb[t][n][e] = transpose8(pack_weights(p0, p1));
           }
       }
       // ---- O += V^T P: dims 16 j + 2 g8 (x = 0, 1) and one further (x = 2, 3)

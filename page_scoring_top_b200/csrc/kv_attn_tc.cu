@@ -24,9 +24,10 @@
 //    a running maximum, a sum and an accumulator of their own (joined at the
 //    item's end), so that neither waits for the other's rescaling; the weights
 //    go back to TMEM as the A operand, over the scores they come from.  The
-//    maximum is a reference that is moved (and the accumulator rescaled) only
-//    when a row exceeds it by 2^8: fp16 holds weights up to 2^8 as exactly as
-//    up to 1.
+//    reference m is the maximum less 7, and moved (and the accumulator rescaled)
+//    only when that exceeds it by 8: weights are at most 2^15, within fp16, and
+//    the largest at least 2^7, so that those down to 2^-21 of it are held to
+//    2^-11 of their own size and smaller ones to 2^-32 of the largest.
 //
 // Measured: 4 requests x 16 tokens x 64 heads over 24-32 k keys 186 us, 2 x 1024
 // tokens x 32 heads over up to 8192 keys 433 us (0.31 PFLOP/s): bound by the chain
@@ -55,7 +56,8 @@ constexpr int kTkHalf = 64;        // keys of a copied stage
 constexpr int kTkStages = 5;       // stages of the rings of K and of V
 constexpr int kTkCharge = 4;       // tiles that an item's start and end count for
 constexpr int kTkMeta = 6;         // tiles whose scales are held: up to five are in the pipeline
-constexpr float kTkSlack = 8.f;    // log2 by which a row may exceed its reference
+constexpr float kTkLift = 7.f;     // log2 of the largest weight when the reference is moved
+constexpr float kTkSlack = 8.f;    // log2 by which a row may exceed that before it is moved again
 constexpr float kTkLarge = 8388608.f;  // exponents from here on take the long way
 
 template <int DP, bool PERKEY>
@@ -668,6 +670,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
         };
         if (all) maxima(std::true_type());
         else maxima(std::false_type());
+        top -= kTkLift;
         const bool move = top > m + kTkSlack || (m == -INFINITY && top > m);
         if (__any_sync(0xFFFFFFFFu, move)) {
           const float m2 = move ? top : m;
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
                 p[0] *= e.rest;
                 p[1] *= e.rest;
               }
-              w[j >> 1] = pack_f16(p[0], p[1]);
+              w[j >> 1] = pack_weights(p[0], p[1]);
             }
             if (!PERKEY) l = fmaf(s0 + s1, e.iv, l);
             tk_st16(s_t + c * 16, w);
