@@ -15,8 +15,10 @@
 // held to 2^-11 of their own size, smaller ones to 2^-39 of the largest (a key
 // with most of the weight and no value, over a long context, leaves the output
 // to them).  e4m3 and int8 codes are exact in fp16, products are exact and sums
-// are fp32.  fp16 holds bf16 queries exactly too, after a power of two per row
-// (its inverse goes into the score's factor).  A value scale below 2^-86 counts
+// are fp32.  bf16 queries become fp16 under a power of two per row that brings the
+// largest element to fp16's top binade (its inverse goes into the score's
+// factor): exact for elements down to 2^-31 of the largest, to 2^-39 of it below.
+// A value scale below 2^-86 counts
 // as 2^-86 in the exponent (the sum l stays finite), and its weights are
 // multiplied by what is left.
 //
@@ -220,6 +222,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t w) {
   uint32_t r;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(w));
   return r;
+}
+
+// The power of two that a row of queries is multiplied by, from the exponent field
+// of its largest finite element (which it brings to [2^14, 2^15), or as near as
+// its own range allows), and its inverse.
+__device__ __forceinline__ void query_factors(int field, float& f, float& inverse) {
+  const int e = field < 15 ? 15 : field;  // at most 254
+  f = __int_as_float((268 - e) << 23);
+  inverse = __int_as_float((e - 14) << 23);
 }
 
 // Four codes of a word as fp16 pairs: (0, 1), (2, 3), or, ACROSS, (0, 2), (1, 3).
@@ -738,9 +749,8 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
         top = lo < 0x7F80u && lo > top ? lo : top;
         top = hi < 0x7F80u && hi > top ? hi : top;
       }
-      int e = (int)(__reduce_max_sync(0xFFFFFFFFu, top) >> 7);  // exponent field of the largest
-      e = e < 1 ? 1 : (e > 252 ? 252 : e);
-      const float f = __int_as_float((254 - e) << 23);  // 2^(127 - e)
+      float f, inverse;
+      query_factors((int)(__reduce_max_sync(0xFFFFFFFFu, top) >> 7), f, inverse);
       uint32_t o[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -749,7 +759,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
         *reinterpret_cast<uint4*>(s_q + m * L::kQPitch + lane * 16) =
             make_uint4(o[0], o[1], o[2], o[3]);
       if (lane == 0) {
-        s_qf[m] = a.scale * 1.44269504088896340736f * __int_as_float(e << 23);
+        s_qf[m] = a.scale * 1.44269504088896340736f * inverse;
         s_lim[m] = qlim[i];
       }
     }

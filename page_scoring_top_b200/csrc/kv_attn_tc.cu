@@ -6,7 +6,8 @@
 // With 128 query rows (tokens x heads of one kv head) a key's codes are used
 // for 128 rows, which is work for the tcgen05 tensor cores: per tile of 128
 // keys S = Q K^T and O += P V, both M = 128, fp16 operands (codes are exact in
-// fp16, bf16 queries after a power of two per row), fp32 accumulators in TMEM.
+// fp16, bf16 queries down to 2^-31 of a row's largest, under a power of two per
+// row), fp32 accumulators in TMEM.
 //
 // What bounds it: at one key head and 128 rows a tile costs 1024 cycles of the
 // tensor cores, 1024 of the exponent unit (128 x 128 at 16 a cycle) and, when
@@ -514,9 +515,8 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             top = hi < 0x7F80u && hi > top ? hi : top;
           }
         }
-        int e = (int)(top >> 7);
-        e = e < 1 ? 1 : (e > 252 ? 252 : e);
-        const float f = __int_as_float((254 - e) << 23);
+        float f, inverse;
+        query_factors((int)(top >> 7), f, inverse);
         unsigned char* row = smem + L::q + m * 128;
 #pragma unroll 4
         for (int i = 0; i < DP / 8; ++i) {  // (again, from the L1)
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
           *reinterpret_cast<uint4*>(row + (i >> 3) * (kTkRows * 128) + ((i & 7) ^ (m & 7)) * 16) =
               make_uint4(o[0], o[1], o[2], o[3]);
         }
-        s_qf[sb + m] = a.scale * 1.44269504088896340736f * __int_as_float(e << 23);
+        s_qf[sb + m] = a.scale * 1.44269504088896340736f * inverse;
         s_lim[sb + m] = use ? kv_count(a, r, bits) : 0;
         fence_proxy_async_smem();
         __syncwarp();

@@ -169,3 +169,35 @@ def test_many_keys_of_zero_scale(ctx):
         want = np.log(c["counts"][0].astype(float))
         assert np.abs(lse.double().cpu().numpy()[0] - want[:, None]).max() < 1e-4
     assert status(ctx) == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("span", [0, 12, 18, 21, 24])
+@pytest.mark.parametrize("floor,shape", KERNELS)
+def test_queries_with_an_element_far_above_the_others(ctx, fmt, span, floor, shape):
+    # one element 2^span above the others, where the keys are zero: the scores are
+    # those of the other elements, which use all of bf16's digits
+    c, rng = make(fmt, keys=700, seed=span, **dict(shape, **({"K": 8} if "K" in shape else {})))
+    n, D = at(c, "kc").shape
+    q = rng.uniform(0.25, 2, c["q64"].shape) * rng.choice([-1, 1], c["q64"].shape)
+    q[..., 5] = 2.0 ** span
+    c["q64"], c["q"] = bf16(q)
+    k = rng.integers(-60, 61, (n, D)).astype(float)
+    k[:, 5] = 0
+    put(c, "kc", ref.encode(k, fmt))
+    put(c, "vc", ref.encode(rng.integers(-100, 101, (n, D)).astype(float), fmt))
+    c["scale"] = float(np.float32(3 / (40 * 1.2 * D ** 0.5)))
+    check(ctx, c, floor)
+
+
+@pytest.mark.parametrize("size", [1e-39, 2.0 ** -130, 1e-36, 2.0 ** -112, 1e-30, 1e30, 3e38])
+@pytest.mark.parametrize("floor,shape", KERNELS)
+def test_queries_at_the_ends_of_their_range(ctx, size, floor, shape):
+    c, rng = make("int8", keys=500, seed=9, **dict(shape, **({"K": 8} if "K" in shape else {})))
+    n, D = at(c, "kc").shape
+    c["q64"], c["q"] = bf16(rng.choice([-1, 0.5, 1], c["q64"].shape) * size)
+    k = rng.integers(-60, 61, (n, D)).astype(float)
+    put(c, "kc", ref.encode(k, "int8"))
+    put(c, "vc", ref.encode(rng.integers(-100, 101, (n, D)).astype(float), "int8"))
+    c["scale"] = float(np.float32(min(3 / (40 * D ** 0.5) / size, 1e38)))
+    check(ctx, c, floor)
