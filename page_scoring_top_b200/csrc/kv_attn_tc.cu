@@ -569,8 +569,8 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             *reinterpret_cast<uint4*>(d + ((c2 ^ (row & 7)) * 16)) = make_uint4(o[0], o[1], o[2], o[3]);
             *reinterpret_cast<uint4*>(d + (((c2 + 1) ^ (row & 7)) * 16)) = make_uint4(o[4], o[5], o[6], o[7]);
           };
-          if (!mixed) {
-#pragma unroll
+          if (!mixed) {  // (rolled: the roles' loops share the instruction cache)
+#pragma unroll 1
             for (int i = 0; i < PC / 2; ++i) {
               int row, pc;
               const uint4 w = place(i, row, pc);
@@ -628,6 +628,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
       const float qf = s_qf[sb + row];
       const int lim = s_lim[sb + row];
       float m = -INFINITY, l = 0.f;
+      bool large = false;  // some row of the warp has a reference of 2^23 or more
       for (; n < n1 && ok; ++n) {
         if ((int)(n & 1) != wg) continue;
         const int t = sg.t0 + (int)(n - n0);
@@ -677,6 +678,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
           const float f = m2 == -INFINITY ? 1.f : ex2(m - m2);
           m = m2;
           l *= f;
+          large = __any_sync(0xFFFFFFFFu, m2 != -INFINITY && fabsf(m2) >= kTkLarge);
           if (n >= n0 + 2) {  // the stream has an accumulator already
             if (!await(&o_done[wg], ((n >> 1) - 1) & 1)) break;
             tc_fence_after();
@@ -733,7 +735,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             tk_st16(s_t + c * 16, w);
           }
         };
-        if (all && !__any_sync(0xFFFFFFFFu, fabsf(z) >= kTkLarge)) weights(std::true_type());
+        if (all && !large) weights(std::true_type());
         else weights(std::false_type());
         tk_st_wait();
         tc_fence_before();
