@@ -234,9 +234,10 @@ typedef enum { IDX_KV_E4M3 = 0, IDX_KV_INT8 = 1 } idx_kv_format;
  *     key_counts[b][t]  = cached[b] + t + 1    (what kv_attention takes),
  *     page_counts[b][t] = ceil(key_counts[b][t] / P)  (the token_lengths of the
  *                         _tokens calls),
- * and -1, 0, 0 for t >= fresh[b].  free_head_out (device int32, may be NULL,
- * must not be free_head) gets the entry after the last one taken: the same
- * call twice with the same inputs gives the same result.
+ * and -1, 0, 0 for t >= fresh[b].  free_head_out (device int32, may be NULL)
+ * gets the entry after the last one taken: the same call twice with the same
+ * inputs gives the same result.  The outputs must not overlap the inputs
+ * (cached, fresh, free_list, free_head): such a call is refused.
  * Reported by idx_get_status: a count outside [0, N*P] (or beyond T, or a
  * free_head outside the list) is clamped (bit 1); a block id outside
  * [0, n_blocks) (bit 4) or a page past the end of the free list (bit 8, its

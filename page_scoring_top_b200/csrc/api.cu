@@ -531,6 +531,12 @@ static int check_cache(const void* k_cache, const void* v_cache, const float* k_
   return IDX_OK;
 }
 
+// Whether n int32 at p and m int32 at q share any (a null pointer has none).
+static bool overlap(const int32_t* p, int64_t n, const int32_t* q, int64_t m) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return p && q && a < b + 4 * (uintptr_t)m && b < a + 4 * (uintptr_t)n;
+}
+
 IDX_API int kv_block_tables(idx_ctx* ctx, const int32_t* cached, const int32_t* fresh, int B, int T,
                             int P, int N, int32_t* page_table, int64_t ld_pt, int n_blocks,
                             const int32_t* free_list, int n_free, const int32_t* free_head,
@@ -544,6 +550,13 @@ IDX_API int kv_block_tables(idx_ctx* ctx, const int32_t* cached, const int32_t* 
   if ((int64_t)N * P > INT32_MAX - P || (int64_t)n_blocks * P > INT32_MAX ||
       (int64_t)B * T > INT32_MAX)
     return IDX_EUNSUPPORTED;
+  // every CTA reads the counts of all requests before its own
+  for (const int32_t* out : {slots, key_counts, page_counts, free_head_out}) {
+    const int64_t n = out == free_head_out ? 1 : (int64_t)B * T;
+    if (overlap(out, n, cached, B) || overlap(out, n, fresh, B) || overlap(out, n, free_list, n_free) ||
+        overlap(out, n, free_head, 1))
+      return IDX_EINVAL;
+  }
   DeviceGuard guard(ctx->device);
   if (!guard.ok()) return IDX_ECUDA;
   idx::KvTablesArgs a{};
