@@ -37,7 +37,7 @@
  *   allocate and never synchronise the host.  One context must not be used on
  *   two streams at once: its workspace is shared by its calls.
  * - Alignment: q, c, scores: 16 bytes; ldc_b*2 bytes a multiple of 16;
- *   D a multiple of 8 and at most 256.
+ *   D a multiple of 8 (KV cache calls: 16) and at most 256.
  * - Return value: IDX_OK or a negative idx_status.  Argument errors are found
  *   on the host before anything is launched.  Length VALUES live on the device
  *   and are not read by the host: a length outside [0, N] is clamped into it on
@@ -64,13 +64,13 @@ typedef struct CUstream_st* idx_stream; /* the same type as cudaStream_t */
 typedef enum {
   IDX_OK = 0,
   IDX_EINVAL = -1,        /* null pointer, non-positive size, bad alignment/stride */
-  IDX_EUNSUPPORTED = -2,  /* shape outside what the kernels handle (D, K limits) */
+  IDX_EUNSUPPORTED = -2,  /* shape outside what the kernels handle (D, K or size limits of the call) */
   IDX_ENOWORKSPACE = -3,  /* rows, N or K beyond the limits given to idx_init */
   IDX_ECUDA = -4,         /* a CUDA runtime call or kernel launch failed */
   IDX_EDEVICE = -5        /* device-side status raised (see idx_get_status) */
 } idx_status;
 
-/* Largest K any call accepts. */
+/* Largest K of the calls that select (the page lists of kv_attention may be longer). */
 #define IDX_MAX_K 2048
 
 /*
@@ -216,7 +216,9 @@ IDX_API int kmeans_scores(idx_ctx* ctx, const uint16_t* x, const uint16_t* centr
  *                     key at position i is row i % P of page i / P
  *   slot              block * P + row of a token, -1 for none
  *
- * D a multiple of 16 and at most 256; n_blocks * H * P and N * P below 2^31.
+ * D a multiple of 16 and at most 256, P at most 65536, H at most 65535;
+ * n_blocks * H * P, B * T and (kv_attention) B * T * Q below 2^31, N * P below
+ * 2^31 - P (kv_attention: and 2^31 - 128).
  * The limits given to idx_init do not bind these calls (kv_attention uses a part
  * of the workspace whose size is fixed; the others use none).  Their batches are
  * [B][T] rows, T tokens per request; a request with fewer is padded (slot -1,

@@ -625,7 +625,10 @@ IDX_API int kv_attention(idx_ctx* ctx, const uint16_t* q, int64_t ldq, const voi
   if (Q % H != 0 || !aligned16(q) || !aligned16(out) || (ldq % 8) != 0 || ldq < (int64_t)Q * D)
     return IDX_EINVAL;
   if (!std::isfinite(scale)) return IDX_EINVAL;
-  if ((int64_t)N * P > INT32_MAX - P || (int64_t)B * T > INT32_MAX / Q) return IDX_EUNSUPPORTED;
+  // positions are ints up to the end of the last page, or tile of 128 keys; so
+  // are list entries up to the end of the last unit
+  if ((int64_t)N * P > INT32_MAX - std::max(P, 128) || K > INT32_MAX - 32 || (int64_t)B * T > INT32_MAX / Q)
+    return IDX_EUNSUPPORTED;
   DeviceGuard guard(ctx->device);
   if (!guard.ok()) return IDX_ECUDA;
   idx::KvAttnArgs a{};
@@ -676,7 +679,8 @@ IDX_API const char* idx_strerror(int code) {
   switch (code) {
     case IDX_OK: return "ok";
     case IDX_EINVAL: return "invalid argument (null pointer, size, alignment or stride)";
-    case IDX_EUNSUPPORTED: return "unsupported shape (D must be a multiple of 8 up to 256; K up to 2048)";
+    case IDX_EUNSUPPORTED: return "unsupported shape (D must be a multiple of 8, of 16 for the KV cache, up to 256; K up to 2048 for "
+           "the selections; or a size limit of the call)";
     case IDX_ENOWORKSPACE: return "rows, N or K exceed the limits given to idx_init";
     case IDX_ECUDA: return "CUDA runtime error or kernel launch failure";
     case IDX_EDEVICE: return "device-side status raised (clamped length or expired wait)";

@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-from test_kv_cpu import BASE, EINVAL, TABLES, TABLES_OK, _call, lib  # noqa: F401  (lib: the fixture)
+from test_kv_cpu import ATTN, ATTN_OK, EINVAL, EUNSUPPORTED, TABLES, TABLES_OK, _call, lib  # noqa: F401  (lib: the fixture)
 
 pytest.importorskip("torch")
 
@@ -26,3 +26,18 @@ def test_block_tables_refuses_outputs_over_its_inputs(lib, out, read, entries): 
         import torch
         if not torch.cuda.is_available():
             assert _call(lib.kv_block_tables, TABLES, APART, **{out: APART[read] + 4 * off}) != EINVAL
+
+
+NEAR = (2 ** 31 - 17) // 16  # pages of 16 that hold the most positions below 2^31 - 16
+
+
+@pytest.mark.parametrize("change", [
+    dict(N=NEAR, ld_pt=NEAR, page_idx=None, K=0), dict(N=NEAR, ld_pt=NEAR), dict(K=2 ** 31 - 20)])
+def test_attention_refuses_positions_that_leave_31_bits(lib, change):  # noqa: F811
+    assert _call(lib.kv_attention, ATTN, ATTN_OK, **change) == EUNSUPPORTED
+
+
+def test_the_text_for_unsupported_shapes_covers_the_cache(lib):  # noqa: F811
+    lib.idx_strerror.restype = ctypes.c_char_p
+    text = lib.idx_strerror(EUNSUPPORTED)
+    assert b"multiple of 8" in text and b"16 for the KV cache" in text and b"limit" in text
