@@ -31,7 +31,7 @@ struct idx_ctx {
   int* status;
   float* scratch;  // fp32 scores for the score-then-select route
   int64_t scratch_elems;
-  float* kv_ws;  // attention over the KV cache: partial results of cut items
+  float* kv_ws;  // attention over the KV cache: partial results of cut items (the same memory)
   int32_t* kv_arrive;
 };
 
@@ -246,8 +246,8 @@ IDX_API int idx_init(idx_ctx** out, int device, int max_rows, int max_n, int max
   const size_t o_arr = carve((size_t)max_rows * 4);
   const size_t o_kva = carve((size_t)sms * 4);
   const size_t o_st = carve(16);
-  const size_t o_scr = carve((size_t)ctx->scratch_elems * 4);
-  const size_t o_kvw = carve(idx::kv_attn_ws_floats(sms) * 4);
+  // Both hold what one call writes and reads: they share their memory.
+  const size_t o_scr = carve(std::max((size_t)ctx->scratch_elems, idx::kv_attn_ws_floats(sms)) * 4);
   ctx->ws_bytes = off;
   char* base = nullptr;
   if (cudaMalloc(&base, off) != cudaSuccess) {
@@ -271,7 +271,7 @@ IDX_API int idx_init(idx_ctx** out, int device, int max_rows, int max_n, int max
   ctx->arrive = reinterpret_cast<int32_t*>(base + o_arr);
   ctx->status = reinterpret_cast<int*>(base + o_st);
   ctx->scratch = reinterpret_cast<float*>(base + o_scr);
-  ctx->kv_ws = reinterpret_cast<float*>(base + o_kvw);
+  ctx->kv_ws = reinterpret_cast<float*>(base + o_scr);
   ctx->kv_arrive = reinterpret_cast<int32_t*>(base + o_kva);
   *out = ctx;
   return IDX_OK;
