@@ -88,7 +88,7 @@ constexpr int kKvCharge = 28;
 constexpr int kKvSegs = 64;        // descriptor ring: more than the stages and a group of warps
 constexpr int kKvSmem = 227 * 1024;
 constexpr float kKvMinScale = 1.2924697071141057e-26f;  // 2^-86
-constexpr float kKvLift = 14.f;  // log2 of the largest weight
+constexpr float kKvLift = 14.f;            // log2 of the largest weight
 
 // What the host settles for a launch.
 struct KvPlan {
@@ -315,6 +315,13 @@ __device__ __forceinline__ KvTile kv_tile(const KvAttnArgs& a, const KvPlan& pl,
 __device__ __forceinline__ int kv_parts(int64_t unit0, int nt, int64_t W, int64_t nc, int64_t& c0) {
   c0 = ((unit0 + 1) * nc + W - 1) / W - 1;
   return (int)(((unit0 + nt) * nc + W - 1) / W - 1 - c0) + 1;
+}
+
+// log(sum_i exp(s_i)) of a row from its reference and sum, whose weights carry
+// 2^LIFT: taken off first, so that the logarithm is of the size of the count.
+template <int LIFT>
+__device__ __forceinline__ float kv_lse(float m, float l) {
+  return (m + (float)LIFT + __log2f(l * (1.f / (1 << LIFT)))) * 0.69314718055994530942f;
 }
 
 // One thread of a CTA is through with its part of such an item, written or not
@@ -1046,7 +1053,7 @@ __global__ void __launch_bounds__(KvLayout<DP, NT, RG, MULTI>::kThreads, 1)
       };
       *reinterpret_cast<uint2*>(a.out + rq * a.D + oc) = make_uint2(two(o.x, o.y), two(o.z, o.w));
       if (oc == 0 && a.lse)
-        a.lse[rq] = zero ? -INFINITY : (m + __log2f(l)) * 0.69314718055994530942f;
+        a.lse[rq] = zero ? -INFINITY : kv_lse<(int)kKvLift>(m, l);
     };
     auto own_factor = [&](float mk, float lk, float m) {  // 0 for no keys, NaN stays
       return mk == -INFINITY ? (lk == lk ? 0.f : lk) : ex2(mk - m);

@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
           wslot[128 * 128 + row] = rm;
           wslot[128 * 128 + 128 + row] = rl;
         } else if (a.lse) {
-          a.lse[rq] = zero ? -INFINITY : (rm + __log2f(rl)) * 0.69314718055994530942f;
+          a.lse[rq] = zero ? -INFINITY : kv_lse<(int)kTkLift>(rm, rl);
         }
       }
       tc_fence_before();
@@ -873,7 +873,7 @@ __global__ void __launch_bounds__(kTkThreads, 1)
             if (col < a.D)
               *reinterpret_cast<uint2*>(a.out + q2 * a.D + col) = make_uint2(pair(o.x, o.y), pair(o.z, o.w));
             if (lane == 0 && a.lse)
-              a.lse[q2] = z2 ? -INFINITY : (m_ + __log2f(l_)) * 0.69314718055994530942f;
+              a.lse[q2] = z2 ? -INFINITY : kv_lse<(int)kTkLift>(m_, l_);
           }
         }
         group_sync(kTkSoft);  // s_flag is read

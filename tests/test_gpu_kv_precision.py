@@ -201,3 +201,16 @@ def test_queries_at_the_ends_of_their_range(ctx, size, floor, shape):
     put(c, "vc", ref.encode(rng.integers(-100, 101, (n, D)).astype(float), "int8"))
     c["scale"] = float(np.float32(min(3 / (40 * D ** 0.5) / size, 1e38)))
     check(ctx, c, floor)
+
+
+@pytest.mark.parametrize("floor,shape", KERNELS)
+def test_lse_of_a_few_equal_scores(ctx, floor, shape):
+    # log(n): a base-2 logarithm below 4 to two fp32 steps of 2^-22, and two roundings
+    shape = dict(shape)
+    shape.pop("K", None)
+    for n in range(1, 16):
+        c, _ = make("int8", keys=64, **shape)
+        c["counts"][:] = n
+        lse = launch_attn(ctx, c)[1].double().cpu().numpy()
+        assert np.abs(lse - np.log(n)).max() <= np.log(2) * 2.0 ** -21 + 2 * 2.0 ** -24 * np.log(n)
+    assert status(ctx) == 0
