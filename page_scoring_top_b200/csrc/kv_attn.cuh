@@ -56,9 +56,9 @@
 //
 // What bounds it: HBM by its bytes (2 D per key and kv head); measured at 32
 // requests x 256 pages of 64 keys, 8 kv heads: D = 128 e4m3 167 us (5.2 TB/s), D =
-// 256 285 us (6.0), D = 64 131 us (3.3): with fewer bytes a unit the
-// consumers' decoding and softmax (about 500 instructions a unit) are what the
-// memory waits for.
+// 256 287 us (6.0), D = 64 129 us (3.4): with fewer bytes a unit the
+// consumers' decoding and softmax are what the memory waits for (570 warp
+// instructions a unit in all roles, 910 at D = 256 and 390 at D = 64).
 #pragma once
 
 #include <cuda.h>

@@ -30,9 +30,11 @@
 //    the largest at least 2^7, so that those down to 2^-21 of it are held to
 //    2^-11 of their own size and smaller ones to 2^-32 of the largest.
 //
-// Measured: 4 requests x 16 tokens x 64 heads over 24-32 k keys 186 us, 2 x 1024
-// tokens x 32 heads over up to 8192 keys 433 us (0.31 PFLOP/s): bound by the chain
-// scores, maximum, weights, product of the two streams (4.1 us for two tiles).
+// Measured: 4 requests x 16 tokens x 64 heads over 24-32 k keys 190 us, 2 x 1024
+// tokens x 32 heads over up to 8192 keys 438 us (0.31 PFLOP/s): bound by the chain
+// scores, maximum, weights, product of the two streams (a tile takes an SM 4.1 us,
+// with two under way) and, in it, by instruction fetch: the same loops with their
+// roles in another order measured 406 to 472 us.
 //
 // TMEM, 512 columns: S0 S1 O0 O1, 128 each; weights in the first half of S.
 // The split over the SMs and the joining of cut items are those of kv_attn.cuh,

@@ -7,11 +7,12 @@
 // every new token and the key and page counts of its attention row.
 //
 // What bounds it: latency (a few kilobytes of lengths, 12 bytes out per
-// token; 5 us for 256 single tokens and for 64 x 1024).  So it is one kernel, without a second pass for the prefix sum:
-// every CTA sums the needs of all requests before its own group (two coalesced
-// loads per request, from the L2) and scans its group in shared memory.  The
-// slots of new pages are read from the free list itself, not from the table
-// entries that the same launch writes.
+// token; 6 us for 256 single tokens and for 64 x 1024, replayed in a graph).
+// So it is one kernel, without a second pass for the prefix sum: every CTA sums
+// the needs of all requests before its own group (two coalesced loads per
+// request, from the L2) and scans its group in shared memory.  The slots of new
+// pages are read from the free list itself, not from the table entries that the
+// same launch writes.
 #include "common.cuh"
 #include "kernels.h"
 
