@@ -288,9 +288,9 @@ IDX_API int kv_append(idx_ctx* ctx, const uint16_t* k, const uint16_t* v, int64_
  * NULL.  Sums and softmax statistics are fp32; the softmax weights times their
  * value scales are rounded once to fp16 for the products with V: to 2^-11 of
  * their own size, and to no less than 2^-39 of the row's largest (2^-32 for more
- * than 64 rows, T * Q/H, that share their keys); a value scale below 2^-86 costs
- * its keys what it is less.  Query elements below 2^-31 of
- * their row's largest are rounded to 2^-39 of it.
+ * than 64 rows, T * Q/H, that share their keys; where the largest value scale of
+ * a row's keys is below 2^-86, those powers are larger by as much).  Query
+ * elements below 2^-31 of their row's largest are rounded to 2^-39 of it.
  * Reported by idx_get_status: a key count outside [0, N*P] is clamped (bit 1);
  * a page_idx entry outside [-1, N) or a block outside [0, n_blocks) is left
  * out (bit 4).

@@ -18,9 +18,8 @@
 // are fp32.  bf16 queries become fp16 under a power of two per row that brings the
 // largest element to fp16's top binade (its inverse goes into the score's
 // factor): exact for elements down to 2^-31 of the largest, to 2^-39 of it below.
-// A value scale below 2^-86 counts
-// as 2^-86 in the exponent (the sum l stays finite), and its weights are
-// multiplied by what is left.
+// A value scale below 2^-86 counts as 2^-86 in the exponent (the sum l stays
+// finite), and its weights are multiplied by what is left.
 //
 // Work: a row tile is TT tokens of one request (1 with page lists, which differ
 // by token) and up to 16*MT query rows (tokens x heads of one kv head), an item
